@@ -351,6 +351,126 @@ int fo_hbm_probe(void* dst, const void* src, int64_t bytes, int32_t mode, int32_
  */
 int fo_selftest(int what, uint32_t lo, uint64_t count, uint64_t* mismatches, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Row operators of a training step: dropout, layer norm, RMS norm, and the
+ * dropout + residual sum + norm in which the two meet.  They run between the
+ * matrix products of a step whose weights the entry points above update: norm
+ * weights may be theta' (bf16 or fp16), and their gradients are written in the
+ * weights' type, which is the one the fused steps read.
+ *
+ * Data is a matrix of `rows` rows of `cols` elements of one type (`dtype`:
+ * FO_BF16, FO_FP16 or FO_F32; elements of a row are consecutive).  Inputs have
+ * a row stride in elements (`*_ld`, >= 0; 0 repeats one row); outputs are
+ * packed (row stride = cols).  rows is at most 2^40, cols at most 2^30.
+ * Differing from the conventions above: rows may begin at any element, so
+ * arrays need only their element's alignment (the workspace 16 bytes), and no
+ * call allocates, synchronises or keeps anything: all may be captured into a
+ * HIP graph.  Outputs must not overlap any other array of the call
+ * (FO_EALIAS; an input's extent runs from its first to its last element).
+ * Arithmetic is float32 whatever the type, and every output is rounded once to
+ * its type (to nearest even).  Results do not depend on the device, the stream
+ * or the order in which workgroups finish.
+ * ------------------------------------------------------------------------ */
+enum fo_dtype { FO_F32 = 2 };       /* element types: FO_BF16, FO_FP16 and this */
+enum fo_norm_kind { FO_LAYER_NORM = 0, FO_RMS_NORM = 1 };
+
+/*
+ * What decides a dropout mask.  Nothing is stored: the mask is a function of
+ * the key, the element's row and column, and cols, so a backward pass given the
+ * same key finds it again.
+ *   p      : drop probability in [0, 1], held as thr = round(2^32 p) / 2^32;
+ *            kept elements are scaled by 1 / (1 - thr); p = 1 drops everything
+ *   seed, offset : any values; use another offset (or seed) for every mask that
+ *            should be independent
+ *   state  : NULL, or 2 uint64 in device memory added to (seed, offset) when
+ *            the kernel runs; a captured graph draws new masks when the caller
+ *            changes them between replays.  They must not change between a
+ *            forward pass and its backward pass.
+ * The decision: chunk b = row * ceil(cols / 8) + column / 8; words
+ * W(b, i) = Philox4x32-10 of counter (b mod 2^32, b / 2^32 + i * 2^31, offset
+ * mod 2^32, offset / 2^32) under key (seed mod 2^32, seed / 2^32); element
+ * j = column mod 8 takes half-word j (low half of word 0 first) of W(b, 0) as
+ * the high and of W(b, 1) as the low 16 bits of u, and is kept if
+ * u >= round(2^32 p).  (Philox: Salmon, Moraes, Dror, Shaw, SC 2011.)
+ */
+typedef struct fo_dropout_key {
+  double          p;
+  uint64_t        seed, offset;
+  const uint64_t* state;
+} fo_dropout_key;
+
+/*
+ * fo_dropout
+ * y = kept ? x / (1 - thr) : 0.  Dropped elements are +0 whatever x holds (NaN
+ * and infinities included).  The gradient is the same call on y's gradient.
+ *   x : rows x cols (read, stride x_ld);  y : rows x cols (written)
+ * rows == 0 or cols == 0 is a no-op.  Errors: FO_EINVAL, FO_EALIAS, FO_EHIP.
+ */
+int fo_dropout(const void* x, int64_t x_ld, void* y, int64_t rows, int64_t cols, int dtype,
+               const fo_dropout_key* key, void* stream);
+
+/* Arguments of fo_norm_forward. */
+typedef struct fo_norm_fwd {
+  const void* x;            /* rows x cols */
+  const void* residual;     /* rows x cols, or NULL */
+  const void* weight;       /* cols of wdtype, or NULL (1) */
+  const void* bias;         /* cols of wdtype, or NULL (0); layer norm only */
+  void*       h;            /* rows x cols (written); with a residual only, and then required */
+  void*       y;            /* rows x cols (written) */
+  float*      mean;         /* rows (written), or NULL; layer norm only */
+  float*      rstd;         /* rows (written), or NULL */
+  int64_t     rows, cols, x_ld, residual_ld;
+  double      eps;          /* finite, >= 0 */
+  fo_dropout_key drop;      /* p must be 0 without a residual */
+  int32_t     dtype, wdtype, kind, reserved;
+} fo_norm_fwd;
+
+/*
+ * fo_norm_forward
+ *   h = residual + dropout(x), rounded to dtype (h = x without a residual)
+ *   m = mean(h) (RMS norm: 0);  r = 1 / sqrt(mean((h - m)^2) + eps)
+ *   y = (h - m) * r * weight + bias
+ * The statistics are taken of the rounded h, from its values less their mean.
+ * rows == 0 is a no-op.  Errors: FO_EINVAL, FO_EALIAS, FO_EHIP.
+ */
+int fo_norm_forward(const fo_norm_fwd* args, void* stream);
+
+/* Arguments of fo_norm_backward. */
+typedef struct fo_norm_bwd {
+  const void*  dy;          /* gradient of y, rows x cols */
+  const void*  dh;          /* gradient of h from elsewhere, rows x cols, or NULL (0) */
+  const void*  h;           /* what was normalised: h, or x without a residual */
+  const void*  weight;      /* as in the forward call */
+  const float* mean;        /* as written by it (layer norm) */
+  const float* rstd;
+  void*        d;           /* gradient of h, and of the residual (written), or NULL */
+  void*        dx;          /* gradient of the dropped-out x (written), or NULL; needs drop.p > 0 */
+  void*        dweight;     /* cols of wdtype (written), or NULL */
+  void*        dbias;       /* cols of wdtype (written), or NULL; layer norm only */
+  void*        workspace;   /* device memory, needed with dweight or dbias */
+  int64_t      workspace_bytes;
+  int64_t      rows, cols, dy_ld, dh_ld, h_ld;
+  fo_dropout_key drop;      /* as in the forward call */
+  int32_t      dtype, wdtype, kind, reserved;
+} fo_norm_bwd;
+
+/*
+ * fo_norm_backward
+ *   g = dy * weight;  u = (h - m) * r
+ *   d = r * (g - mean(g) - u * mean(g * u)) + dh    (RMS norm: no mean(g))
+ *   dx = kept ? d / (1 - thr) : 0
+ *   dweight = sum over rows of dy * u;  dbias = sum over rows of dy
+ * The sums over rows are float32, in an order that depends on the sizes alone.
+ * rows == 0 writes zero weight gradients.  The workspace is scratch: its
+ * contents before and after a call mean nothing, and two calls that may run at
+ * the same time need two.  Errors: FO_EINVAL, FO_EALIAS, FO_EHIP.
+ */
+int fo_norm_backward(const fo_norm_bwd* args, void* stream);
+
+/* Bytes of workspace fo_norm_backward needs for weight gradients of a matrix
+ * of this size.  Host-only query.  Errors: FO_EINVAL. */
+int fo_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
 /* Number of launch-table cache slots pinned by calls made under HIP graph
  * capture (all devices).  Host-only query; never fails. */
 int fo_cache_pinned(void);

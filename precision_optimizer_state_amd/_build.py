@@ -6,7 +6,8 @@ import subprocess
 import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
-SRC = os.path.join(PKG, "csrc", "fo_lib.hip")
+SRC = os.path.join(PKG, "csrc", "fo_lib.hip")          # the optimizer step
+ROWS_SRC = os.path.join(PKG, "csrc", "fo_rows.hip")     # the row operators
 OUT_DIR = os.path.join(PKG, "lib")
 OUT = os.path.join(OUT_DIR, "libfoamd.so")
 
@@ -24,17 +25,30 @@ FLAGS = [
 
 
 def build(verbose: bool = False, extra=()) -> str:
+    """Compile the translation units side by side and link them into
+    lib/libfoamd.so."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    flags = [f for f in FLAGS if f != "-shared"]
+    jobs = []
+    for src in (SRC, ROWS_SRC):
+        obj = os.path.join(OUT_DIR, os.path.basename(src)[:-4] + ".o")
+        cmd = ["/opt/rocm/bin/hipcc", *flags, *extra, "-c", src, "-o", obj]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        jobs.append((obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    logs = [job.communicate()[0] for _, job in jobs]
+    for (_, job), log in zip(jobs, logs):
+        if job.returncode != 0:
+            sys.stderr.write(log)
+            raise RuntimeError("hipcc failed building libfoamd.so")
+        if verbose and log.strip():
+            print("\n".join(l for l in log.splitlines() if "packed-fp32-ops" not in l)[:4000])
     tmp = OUT + ".tmp"
-    cmd = ["/opt/rocm/bin/hipcc", *FLAGS, *extra, SRC, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    res = subprocess.run(["/opt/rocm/bin/hipcc", *FLAGS, *[obj for obj, _ in jobs], "-o", tmp],
+                         capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building libfoamd.so")
-    if verbose and res.stderr.strip():
-        print("\n".join(l for l in res.stderr.splitlines() if "packed-fp32-ops" not in l)[:4000])
+        raise RuntimeError("hipcc failed linking libfoamd.so")
     os.replace(tmp, OUT)
     return OUT
 

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_double, c_int, c_int32, c_int64, c_uint32, c_void_p
+from ctypes import c_double, c_int, c_int32, c_int64, c_uint32, c_uint64, c_void_p
 from typing import Iterable, Mapping, Sequence
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libfoamd.so")
@@ -19,17 +19,22 @@ FO_OK, FO_EINVAL, FO_EALIAS, FO_EHIP, FO_ENOMEM = 0, -1, -2, -3, -4
 FO_BF16, FO_FP16 = 0, 1
 FO_COMPANDED, FO_LINEAR, FO_COMPANDED4, FO_COMPANDED_BF16SCALE = 0, 1, 2, 3
 FO_MOMENTUM, FO_VARIANCE = 0, 1
+FO_F32 = 2                                  # element types of the row operators: FO_BF16, FO_FP16, FO_F32
+FO_LAYER_NORM, FO_RMS_NORM = 0, 1
 
-EXPORTS = (
+_STEP_EXPORTS = (
     "fo_split_weights", "fo_reconstruct_weights", "fo_companded_quantize", "fo_dequantize",
     "fo_fused_adamw_step", "fo_fused_adamw_step_noalloc", "fo_fused_sgdm_step", "fo_stream_probe", "fo_hbm_probe",
     "fo_selftest", "fo_cache_pinned", "fo_last_error", "fo_abi_version",
 )
+_ROW_EXPORTS = ("fo_dropout", "fo_norm_forward", "fo_norm_backward", "fo_norm_backward_workspace")
+EXPORTS = _STEP_EXPORTS + _ROW_EXPORTS
 
 WFMT = {"bf16": FO_BF16, "fp16": FO_FP16}
 CODEC = {"companded": FO_COMPANDED, "linear": FO_LINEAR, "companded4": FO_COMPANDED4,
          "companded_bf16scale": FO_COMPANDED_BF16SCALE}
 KIND = {"m": FO_MOMENTUM, "v": FO_VARIANCE}
+NORM = {"layer": FO_LAYER_NORM, "rms": FO_RMS_NORM}
 
 
 class FoError(RuntimeError):
@@ -60,6 +65,27 @@ class SGDMHParams(ctypes.Structure):
                 ("nesterov", c_int32)]
 
 
+class DropoutKey(ctypes.Structure):
+    _fields_ = [("p", c_double), ("seed", c_uint64), ("offset", c_uint64), ("state", c_void_p)]
+
+
+class NormFwd(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("residual", c_void_p), ("weight", c_void_p), ("bias", c_void_p),
+                ("h", c_void_p), ("y", c_void_p), ("mean", c_void_p), ("rstd", c_void_p),
+                ("rows", c_int64), ("cols", c_int64), ("x_ld", c_int64), ("residual_ld", c_int64),
+                ("eps", c_double), ("drop", DropoutKey),
+                ("dtype", c_int32), ("wdtype", c_int32), ("kind", c_int32), ("reserved", c_int32)]
+
+
+class NormBwd(ctypes.Structure):
+    _fields_ = [("dy", c_void_p), ("dh", c_void_p), ("h", c_void_p), ("weight", c_void_p),
+                ("mean", c_void_p), ("rstd", c_void_p), ("d", c_void_p), ("dx", c_void_p),
+                ("dweight", c_void_p), ("dbias", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_int64),
+                ("rows", c_int64), ("cols", c_int64), ("dy_ld", c_int64), ("dh_ld", c_int64), ("h_ld", c_int64),
+                ("drop", DropoutKey),
+                ("dtype", c_int32), ("wdtype", c_int32), ("kind", c_int32), ("reserved", c_int32)]
+
+
 _lib = None
 ABI_VERSION = 6          # FO_ABI_VERSION of include/foamd.h (struct layouts below)
 
@@ -84,7 +110,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fo_stream_probe.argtypes = [ctypes.POINTER(AdamWTensor), c_int32, c_int32, c_int32, c_uint32, P]
     lib.fo_hbm_probe.argtypes = [P, P, c_int64, c_int32, c_int32, c_uint32, P]
     lib.fo_selftest.argtypes = [c_int, c_uint32, ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64), P]
-    for name in EXPORTS:
+    for name in _STEP_EXPORTS:
         getattr(lib, name).restype = c_int
     lib.fo_cache_pinned.argtypes = []
     lib.fo_last_error.restype = ctypes.c_char_p
@@ -93,7 +119,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if lib.fo_abi_version() != ABI_VERSION:
         raise ImportError(f"{path} implements C ABI version {lib.fo_abi_version()}, this binding needs "
                           f"{ABI_VERSION}: rebuild it with __graft_entry__.build()")
+    # the row operators came without a change to the entry points above: a
+    # library of this ABI version that lacks them still steps optimizers
+    if all(hasattr(lib, name) for name in _ROW_EXPORTS):
+        lib.fo_dropout.argtypes = [P, c_int64, P, c_int64, c_int64, c_int, ctypes.POINTER(DropoutKey), P]
+        lib.fo_norm_forward.argtypes = [ctypes.POINTER(NormFwd), P]
+        lib.fo_norm_backward.argtypes = [ctypes.POINTER(NormBwd), P]
+        lib.fo_norm_backward_workspace.argtypes = [c_int64, c_int64, ctypes.POINTER(c_int64)]
+        for name in _ROW_EXPORTS:
+            getattr(lib, name).restype = c_int
     _lib = lib
+    return lib
+
+
+def _load_rows() -> ctypes.CDLL:
+    lib = load()
+    if not hasattr(lib, "fo_norm_forward"):
+        raise ImportError(f"{LIB_PATH} has no row operators: rebuild it with __graft_entry__.build()")
     return lib
 
 
@@ -256,6 +298,127 @@ def fo_stream_probe(tlist, wfmt="bf16", ecc_bits=8, key=0, stream=None) -> None:
         tlist = AdamWList(tlist)
     _check(load().fo_stream_probe(tlist.array, len(tlist), _fmt(wfmt, WFMT), int(ecc_bits), int(key),
                                   _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# row operators: dropout, layer norm, RMS norm, dropout + residual + norm
+# ---------------------------------------------------------------------------
+_DTYPE_NAMES = {"torch.bfloat16": FO_BF16, "torch.float16": FO_FP16, "torch.float32": FO_F32}
+
+
+def _dtype(t) -> int:
+    d = _DTYPE_NAMES.get(str(t.dtype))
+    if d is None:
+        raise ValueError(f"tensors of {t.dtype} are not supported (bfloat16, float16 or float32)")
+    return d
+
+
+def _rows_in(name, t, shape=None, dtype=None):
+    """(address, row stride) of a 2-D input whose rows are consecutive elements."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix (rows, cols), got shape {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {name} must be consecutive")
+    return _addr(t), t.stride(0)
+
+
+def _rows_out(name, t, shape, dtype):
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    return _ptr(t)
+
+
+def _vec(name, t, n, dtype):
+    return _rows_out(name, t, (n,), dtype)
+
+
+def _addr(t) -> c_void_p:
+    """_ptr without its demand for contiguity."""
+    if t.is_contiguous():
+        return _ptr(t)
+    return _ptr(t.as_strided((1,), (1,)))
+
+
+def dropout_key(p, seed, offset=0, state=None) -> DropoutKey:
+    """The key of a dropout mask: drop probability, 64-bit seed and offset, and
+    optionally 2 int64 of device memory added to them when the kernel runs."""
+    if state is not None:
+        import torch
+        if state.dtype != torch.int64 or state.numel() != 2:
+            raise ValueError("the dropout state must hold 2 int64")
+        state = _ptr(state).value
+    return DropoutKey(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1), state)
+
+
+_NO_DROPOUT = DropoutKey(0.0, 0, 0, None)
+
+
+def fo_dropout(x, y_out, key, stream=None) -> None:
+    """x, y_out: (rows, cols) of one type; key: DropoutKey (see dropout_key)."""
+    ptr, ld = _rows_in("x", x)
+    out = _rows_out("y_out", y_out, x.shape, x.dtype)
+    _check(_load_rows().fo_dropout(ptr, ld, out, x.shape[0], x.shape[1], _dtype(x), ctypes.byref(key),
+                                   _stream(stream)))
+
+
+def fo_norm_forward(x, y_out, kind="layer", weight=None, bias=None, eps=1e-5, residual=None, h_out=None,
+                    mean_out=None, rstd_out=None, drop=None, stream=None) -> None:
+    """y_out = norm(h) * weight + bias with h = x, or h_out = residual + dropout(x).
+    Matrices are (rows, cols) of one type, weight and bias (cols,) of another or
+    the same one, mean_out and rstd_out (rows,) float32; drop: DropoutKey."""
+    shape, dt = x.shape, x.dtype
+    xp, x_ld = _rows_in("x", x)
+    rp, r_ld = _rows_in("residual", residual, shape, dt)
+    import torch
+    param = weight if weight is not None else bias
+    wdt = param.dtype if param is not None else dt
+    a = NormFwd(xp, rp, _vec("weight", weight, shape[1], wdt), _vec("bias", bias, shape[1], wdt),
+                _rows_out("h_out", h_out, shape, dt), _rows_out("y_out", y_out, shape, dt),
+                _vec("mean_out", mean_out, shape[0], torch.float32), _vec("rstd_out", rstd_out, shape[0], torch.float32),
+                shape[0], shape[1], x_ld, r_ld, float(eps), drop or _NO_DROPOUT,
+                _dtype(x), _dtype(param) if param is not None else _dtype(x), _fmt(kind, NORM), 0)
+    _check(_load_rows().fo_norm_forward(ctypes.byref(a), _stream(stream)))
+
+
+def fo_norm_backward_workspace(rows: int, cols: int) -> int:
+    out = c_int64(0)
+    _check(_load_rows().fo_norm_backward_workspace(int(rows), int(cols), ctypes.byref(out)))
+    return out.value
+
+
+def fo_norm_backward(dy, h, rstd, kind="layer", mean=None, weight=None, dh=None, d_out=None, dx_out=None,
+                     dweight_out=None, dbias_out=None, workspace=None, drop=None, stream=None) -> None:
+    """The gradients of fo_norm_forward (h: what it normalised).  d_out is the
+    gradient of h (and of the residual), dx_out that of the dropped-out x.
+    `workspace` holds fo_norm_backward_workspace(rows, cols) bytes (allocated
+    here when a weight gradient is asked for and none is given)."""
+    import torch
+    shape, dt = h.shape, h.dtype
+    hp, h_ld = _rows_in("h", h)
+    dyp, dy_ld = _rows_in("dy", dy, shape, dt)
+    dhp, dh_ld = _rows_in("dh", dh, shape, dt)
+    param = next((t for t in (weight, dweight_out, dbias_out) if t is not None), None)
+    wdt = param.dtype if param is not None else dt
+    if workspace is None and (dweight_out is not None or dbias_out is not None):
+        if stream is not None:      # torch would hand the memory on in its own stream's order
+            raise ValueError("a call on a stream given by hand needs a workspace of its own")
+        workspace = torch.empty(fo_norm_backward_workspace(*shape), dtype=torch.uint8, device=h.device)
+    a = NormBwd(dyp, dhp, hp, _vec("weight", weight, shape[1], wdt),
+                _vec("mean", mean, shape[0], torch.float32), _vec("rstd", rstd, shape[0], torch.float32),
+                _rows_out("d_out", d_out, shape, dt), _rows_out("dx_out", dx_out, shape, dt),
+                _vec("dweight_out", dweight_out, shape[1], wdt), _vec("dbias_out", dbias_out, shape[1], wdt),
+                _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                shape[0], shape[1], dy_ld, dh_ld, h_ld, drop or _NO_DROPOUT,
+                _dtype(h), _dtype(param) if param is not None else _dtype(h), _fmt(kind, NORM), 0)
+    _check(_load_rows().fo_norm_backward(ctypes.byref(a), _stream(stream)))
 
 
 HBM_PROBE_MODES = {"read": 0, "write": 1, "copy": 2, "inplace": 3}

@@ -19,17 +19,16 @@
 #include <vector>
 
 #include "../../include/foamd.h"
+#include "fo_error.hpp"
 #include "fo_kernels.hpp"
 #include "fo_slots.hpp"
 #include "fo_grad16.hpp"
 
 using namespace fo;
 
-namespace {
+static thread_local std::string g_err;
 
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...) {
+int fo::fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -38,6 +37,10 @@ int fail(int code, const char* fmt, ...) {
   g_err = buf;
   return code;
 }
+
+void fo::clear_error() { g_err.clear(); }
+
+namespace {
 
 int hip_fail(hipError_t e, const char* what) {
   return fail(FO_EHIP, "%s: %s", what, hipGetErrorString(e));

@@ -1,0 +1,222 @@
+// fo_rows.hip -- C ABI of the row operators (dropout, layer norm, RMS norm and
+// their fused form; see include/foamd.h for the contract of every entry
+// point).  Host work is argument validation and launches; nothing here
+// allocates, synchronises, keeps state between calls or throws.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/foamd.h"
+#include "fo_error.hpp"
+#include "fo_rows_kernels.hpp"
+
+using namespace fo;
+using namespace fo::rows;
+
+namespace {
+
+constexpr int64_t kMaxCols = int64_t(1) << 30;     // a column index plus one launch step stays in 32 bits
+constexpr int64_t kMaxRows = int64_t(1) << 40;
+constexpr int64_t kMaxGrid = int64_t(1) << 30;
+
+size_t elem_size(int dtype) { return dtype == FO_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype == FO_BF16 || dtype == FO_FP16 || dtype == FO_F32; }
+
+int shape_ok(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > kMaxRows) return fail(FO_EINVAL, "rows = %lld is not in [0, 2^40]", (long long)rows);
+  if (cols < 1 || cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^30]", (long long)cols);
+  return FO_OK;
+}
+
+// The arrays of one call: checked one by one, then the outputs against all.
+struct Arrays {
+  struct Span { uintptr_t lo, hi; bool out; const char* name; };
+  Span s[16];
+  int n = 0;
+
+  // `rows` rows of `cols` elements of `size` bytes, `ld` elements apart
+  int add(const void* p, const char* name, bool out, bool required, int64_t rows, int64_t cols, int64_t ld, size_t size,
+          size_t align = 0) {
+    if (!p) return required ? fail(FO_EINVAL, "%s is NULL", name) : FO_OK;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (a % (align ? align : size)) return fail(FO_EINVAL, "%s is not %zu-byte aligned", name, align ? align : size);
+    if (ld < 0) return fail(FO_EINVAL, "the row stride of %s is negative", name);
+    const unsigned __int128 bytes = ((unsigned __int128)(rows > 0 ? rows - 1 : 0) * (uint64_t)ld + (uint64_t)cols) * size;
+    if (bytes > (unsigned __int128)(UINTPTR_MAX - a) || bytes >> 62)
+      return fail(FO_EINVAL, "%s does not fit the address space", name);
+    if (rows > 0) s[n++] = {a, a + (uintptr_t)bytes, out, name};
+    return FO_OK;
+  }
+
+  int disjoint() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j)
+        if ((s[i].out || s[j].out) && s[i].lo < s[j].hi && s[j].lo < s[i].hi)
+          return fail(FO_EALIAS, "%s and %s overlap", s[i].name, s[j].name);
+    return FO_OK;
+  }
+};
+
+#define FO_TRY(expr) do { const int rc_ = (expr); if (rc_) return rc_; } while (0)
+
+int drop_args(const fo_dropout_key* key, DropArgs* d) {
+  if (!(key->p >= 0.0 && key->p <= 1.0)) return fail(FO_EINVAL, "the drop probability must lie in [0, 1]");
+  if (reinterpret_cast<uintptr_t>(key->state) % 8) return fail(FO_EINVAL, "key.state is not 8-byte aligned");
+  const double two32 = 4294967296.0, t = std::nearbyint(key->p * two32);
+  d->all = t >= two32;
+  d->thr = d->all ? 0xffffffffu : (uint32_t)t;
+  d->scale = d->all ? 0.0f : (float)(two32 / (two32 - t));
+  d->seed = key->seed;
+  d->offset = key->offset;
+  d->state = key->state;
+  return FO_OK;
+}
+
+int launch_check(const char* what) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? FO_OK : fail(FO_EHIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+unsigned grid_of(int64_t want) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, kMaxGrid)); }
+
+#define FO_BY_TYPE(dtype, KERNEL, ...)                                     \
+  do {                                                                     \
+    if ((dtype) == FO_BF16) hipLaunchKernelGGL(KERNEL<Bf16>, __VA_ARGS__); \
+    else if ((dtype) == FO_FP16) hipLaunchKernelGGL(KERNEL<Fp16>, __VA_ARGS__); \
+    else hipLaunchKernelGGL(KERNEL<F32>, __VA_ARGS__);                     \
+  } while (0)
+
+// Row ranges the weight gradients are summed over before the ranges are added:
+// the same for a given matrix on every device, so the order of the sums is too.
+int param_splits(int64_t rows, int64_t cols) {
+  return (int)std::min<int64_t>((rows + 7) / 8, 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fo_dropout(const void* x, int64_t x_ld, void* y, int64_t rows, int64_t cols, int dtype, const fo_dropout_key* key,
+               void* stream) {
+  clear_error();
+  if (!key) return fail(FO_EINVAL, "key is NULL");
+  if (!dtype_ok(dtype)) return fail(FO_EINVAL, "bad element type %d", dtype);
+  if (rows == 0 || cols == 0) return rows < 0 || cols < 0 ? fail(FO_EINVAL, "negative size") : FO_OK;
+  FO_TRY(shape_ok(rows, cols));
+  DropoutArgs a = {};
+  FO_TRY(drop_args(key, &a.drop));
+  Arrays ar;
+  FO_TRY(ar.add(x, "x", false, true, rows, cols, x_ld, elem_size(dtype)));
+  FO_TRY(ar.add(y, "y", true, true, rows, cols, cols, elem_size(dtype)));
+  FO_TRY(ar.disjoint());
+  a.x = x; a.y = y; a.rows = rows; a.x_ld = x_ld; a.cols = (int)cols;
+  const int64_t chunks = rows * ((cols + 7) / 8);
+  FO_BY_TYPE(dtype, k_dropout, grid_of((chunks + BLOCK - 1) / BLOCK), BLOCK, 0, static_cast<hipStream_t>(stream), a);
+  return launch_check("dropout launch");
+}
+
+int fo_norm_forward(const fo_norm_fwd* in, void* stream) {
+  clear_error();
+  if (!in) return fail(FO_EINVAL, "args is NULL");
+  if (!dtype_ok(in->dtype) || !dtype_ok(in->wdtype)) return fail(FO_EINVAL, "bad element type");
+  if (in->kind != FO_LAYER_NORM && in->kind != FO_RMS_NORM) return fail(FO_EINVAL, "bad norm kind %d", in->kind);
+  FO_TRY(shape_ok(in->rows, in->cols));
+  if (!(in->eps >= 0.0 && std::isfinite(in->eps))) return fail(FO_EINVAL, "eps must be finite and >= 0");
+  const bool rms = in->kind == FO_RMS_NORM;
+  if (rms && (in->bias || in->mean)) return fail(FO_EINVAL, "an RMS norm has no bias and no mean");
+  FwdArgs a = {};
+  FO_TRY(drop_args(&in->drop, &a.drop));
+  a.dropping = a.drop.thr != 0;
+  // (with no rows every array may be NULL: nothing is read or written)
+  if (in->rows > 0 && !in->residual && (in->h || in->drop.p != 0.0))
+    return fail(FO_EINVAL, "h and dropout need a residual");
+  const int64_t rows = in->rows, cols = in->cols;
+  const size_t es = elem_size(in->dtype), ws = elem_size(in->wdtype);
+  const bool any = rows > 0;
+  Arrays ar;
+  FO_TRY(ar.add(in->x, "x", false, any, rows, cols, in->x_ld, es));
+  FO_TRY(ar.add(in->residual, "residual", false, false, rows, cols, in->residual_ld, es));
+  FO_TRY(ar.add(in->weight, "weight", false, false, 1, cols, 0, ws));
+  FO_TRY(ar.add(in->bias, "bias", false, false, 1, cols, 0, ws));
+  FO_TRY(ar.add(in->h, "h", true, any && in->residual, rows, cols, cols, es));
+  FO_TRY(ar.add(in->y, "y", true, any, rows, cols, cols, es));
+  FO_TRY(ar.add(in->mean, "mean", true, false, rows, 1, 1, 4));
+  FO_TRY(ar.add(in->rstd, "rstd", true, false, rows, 1, 1, 4));
+  FO_TRY(ar.disjoint());
+  if (!any) return FO_OK;
+  a.x = in->x; a.residual = in->residual; a.weight = in->weight; a.bias = in->bias;
+  a.h = in->h; a.y = in->y; a.mean = in->mean; a.rstd = in->rstd;
+  a.rows = rows; a.x_ld = in->x_ld; a.residual_ld = in->residual_ld;
+  a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms;
+  a.eps = (float)in->eps; a.inv_cols = (float)(1.0 / (double)cols);
+  FO_BY_TYPE(in->dtype, k_norm_fwd_long, grid_of(rows), BLOCK, 0, static_cast<hipStream_t>(stream), a);
+  return launch_check("norm forward launch");
+}
+
+int fo_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
+  FO_TRY(shape_ok(rows, cols));
+  *bytes = 2 * (int64_t)param_splits(rows, cols) * cols * (int64_t)sizeof(float);
+  return FO_OK;
+}
+
+int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
+  clear_error();
+  if (!in) return fail(FO_EINVAL, "args is NULL");
+  if (!dtype_ok(in->dtype) || !dtype_ok(in->wdtype)) return fail(FO_EINVAL, "bad element type");
+  if (in->kind != FO_LAYER_NORM && in->kind != FO_RMS_NORM) return fail(FO_EINVAL, "bad norm kind %d", in->kind);
+  FO_TRY(shape_ok(in->rows, in->cols));
+  const bool rms = in->kind == FO_RMS_NORM;
+  if (rms && (in->dbias || in->mean)) return fail(FO_EINVAL, "an RMS norm has no bias and no mean");
+  BwdArgs a = {};
+  FO_TRY(drop_args(&in->drop, &a.drop));
+  a.dropping = a.drop.thr != 0;
+  if (in->dx && in->drop.p == 0.0) return fail(FO_EINVAL, "dx is for dropout: without it the gradient is d");
+  const int64_t rows = in->rows, cols = in->cols;
+  const size_t es = elem_size(in->dtype), ws = elem_size(in->wdtype);
+  const bool any = rows > 0, params = in->dweight || in->dbias, grads = in->d || in->dx;
+  const int splits = param_splits(rows, cols);
+  Arrays ar;
+  FO_TRY(ar.add(in->dy, "dy", false, any, rows, cols, in->dy_ld, es));
+  FO_TRY(ar.add(in->dh, "dh", false, false, rows, cols, in->dh_ld, es));
+  FO_TRY(ar.add(in->h, "h", false, any, rows, cols, in->h_ld, es));
+  FO_TRY(ar.add(in->weight, "weight", false, false, 1, cols, 0, ws));
+  FO_TRY(ar.add(in->mean, "mean", false, any && !rms, rows, 1, 1, 4));
+  FO_TRY(ar.add(in->rstd, "rstd", false, any, rows, 1, 1, 4));
+  FO_TRY(ar.add(in->d, "d", true, false, rows, cols, cols, es));
+  FO_TRY(ar.add(in->dx, "dx", true, false, rows, cols, cols, es));
+  FO_TRY(ar.add(in->dweight, "dweight", true, false, 1, cols, 0, ws));
+  FO_TRY(ar.add(in->dbias, "dbias", true, false, 1, cols, 0, ws));
+  if (params && any) {
+    const int64_t need = 2 * (int64_t)splits * cols * (int64_t)sizeof(float);
+    if (in->workspace_bytes < need)
+      return fail(FO_EINVAL, "the workspace holds %lld bytes, %lld are needed", (long long)in->workspace_bytes,
+                  (long long)need);
+    FO_TRY(ar.add(in->workspace, "workspace", true, true, 1, need, 0, 1, 16));
+  }
+  FO_TRY(ar.disjoint());
+  a.dy = in->dy; a.dh = in->dh; a.h = in->h; a.weight = in->weight; a.mean = in->mean; a.rstd = in->rstd;
+  a.d = in->d; a.dx = in->dx; a.partial = (float*)in->workspace;
+  a.rows = rows; a.dy_ld = in->dy_ld; a.dh_ld = in->dh_ld; a.h_ld = in->h_ld;
+  a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms; a.splits = splits;
+  a.inv_cols = (float)(1.0 / (double)cols);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (any && grads) {
+    FO_BY_TYPE(in->dtype, k_norm_bwd_rows_long, grid_of(rows), BLOCK, 0, s, a);
+    FO_TRY(launch_check("norm backward launch"));
+  }
+  if (params) {
+    if (any) {
+      FO_BY_TYPE(in->dtype, k_norm_bwd_cols_long, dim3((unsigned)((cols + 255) / 256), (unsigned)splits), BLOCK, 0, s, a);
+      FO_TRY(launch_check("weight gradient launch"));
+    }
+    ReduceArgs r = {(const float*)in->workspace, in->dweight, in->dbias, (int)cols, any ? splits : 0, in->wdtype};
+    hipLaunchKernelGGL(k_norm_bwd_reduce, dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, s, r);
+    FO_TRY(launch_check("weight gradient sum launch"));
+  }
+  return FO_OK;
+}
+
+}  // extern "C"
