@@ -1,5 +1,5 @@
-"""Build the HIP library in-tree (gfx950), and the drop-in optimizers' host
-marshalling extension.  Used by __graft_entry__.build()."""
+"""Build the HIP library in-tree (gfx950), and the host extensions of the
+drop-in optimizers and of the row operators.  Used by __graft_entry__.build()."""
 
 import os
 import subprocess
@@ -57,9 +57,8 @@ MARSHAL_SRC = os.path.join(PKG, "csrc", "fo_marshal.cpp")
 MARSHAL_OUT = os.path.join(OUT_DIR, "fo_marshal.so")
 
 
-def build_marshal(verbose: bool = False, out: str = MARSHAL_OUT) -> str:
-    """Compile csrc/fo_marshal.cpp (host C++, torch headers) into `out`
-    (lib/fo_marshal.so) with the flags torch's own C++ extensions use."""
+def _build_extension(src, name, out, includes=(), libs=(), verbose=False):
+    """Compile one host C++ extension with the flags torch's own C++ extensions use."""
     import sysconfig
 
     import torch
@@ -70,25 +69,43 @@ def build_marshal(verbose: bool = False, out: str = MARSHAL_OUT) -> str:
     libdirs = ce.library_paths()
     # the defines are those torch.utils.cpp_extension.CppExtension passes for
     # this (ROCm) build of torch, so its headers see the configuration they
-    # were built with; the source itself is host C++ with no GPU code
+    # were built with; the sources themselves are host C++ with no GPU code
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=fo_marshal",
+           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-DTORCH_EXTENSION_NAME={name}",
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            *[f"-I{d}" for d in ce.include_paths()], f"-I{sysconfig.get_paths()['include']}",
-           MARSHAL_SRC, "-o", tmp,
+           *[f"-I{d}" for d in includes], src, "-o", tmp,
            *[f"-L{d}" for d in libdirs], *[f"-Wl,-rpath,{d}" for d in libdirs],
-           "-lc10", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+           *libs, "-lc10", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("g++ failed building fo_marshal.so")
+        raise RuntimeError(f"g++ failed building {os.path.basename(out)}")
     os.replace(tmp, out)
     return out
+
+
+def build_marshal(verbose: bool = False, out: str = MARSHAL_OUT) -> str:
+    """Compile csrc/fo_marshal.cpp (host C++, torch headers) into `out`
+    (lib/fo_marshal.so)."""
+    return _build_extension(MARSHAL_SRC, "fo_marshal", out, verbose=verbose)
+
+
+ROWS_TORCH_SRC = os.path.join(PKG, "csrc", "fo_rows_torch.cpp")
+ROWS_TORCH_OUT = os.path.join(OUT_DIR, "fo_rows_torch.so")
+
+
+def build_rows_torch(verbose: bool = False) -> str:
+    """Compile csrc/fo_rows_torch.cpp (host C++: autograd of the row operators)
+    into lib/fo_rows_torch.so, linked to the libfoamd.so beside it."""
+    return _build_extension(ROWS_TORCH_SRC, "fo_rows_torch", ROWS_TORCH_OUT, ["/opt/rocm/include"],
+                            [f"-L{OUT_DIR}", "-l:libfoamd.so", "-Wl,-rpath,$ORIGIN", "-lc10_hip"], verbose)
 
 
 if __name__ == "__main__":
     print(build(verbose=True))
     print(build_marshal(verbose=True))
+    print(build_rows_torch(verbose=True))

@@ -14,7 +14,8 @@ a function of a seed, an offset and the element's place, and is found again).
 
 All arithmetic runs in the HIP library (fo_dropout, fo_norm_forward,
 fo_norm_backward in include/foamd.h, which defines the formulas and the mask);
-this module marshals tensors and records the autograd graph.  Tensors must live
+a host extension (csrc/fo_rows_torch.cpp) marshals tensors and records the
+autograd graph.  Tensors must live
 on the current GPU; calls go to torch's current stream, allocate only through
 torch and never synchronise, so they can be captured into HIP graphs.  Norms
 are over the last dimension.  Inputs whose rows are not consecutive elements at
@@ -23,59 +24,32 @@ a constant distance are copied first.  Gradients of gradients are not provided.
 
 from __future__ import annotations
 
+import importlib.util
+import os
+
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
-
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """t as (rows, cols), cols its last dimension: a view where the strides allow one."""
-    if t.dim() == 0:
-        return t.view(1, 1)
-    cols = t.shape[-1]
-    if t.stride(-1) != 1 and cols > 1:
-        t = t.contiguous()
-    shape = (t.numel() // cols if cols else 0, cols)
-    try:
-        return t.view(shape)
-    except RuntimeError:
-        return t.contiguous().view(shape)
+EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "fo_rows_torch.so")
+_ext = None
+_M64 = (1 << 64) - 1
 
 
-def _flat(t):
-    return None if t is None else t.contiguous()
-
-
-def _check_p(p: float) -> float:
-    if not 0.0 <= p <= 1.0:
-        raise ValueError(f"the drop probability must lie in [0, 1], got {p}")
-    return float(p)
-
-
-# ---------------------------------------------------------------------------
-# dropout
-# ---------------------------------------------------------------------------
-def _drop(x, key):
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if x.numel():
-        xr = _rows(x)
-        B.fo_dropout(xr, y.view(xr.shape), key)
-    return y
-
-
-class _Dropout(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, p, seed, offset, state):
-        ctx.save_for_backward(state)
-        ctx.args = (p, seed, offset)
-        return _drop(x, B.dropout_key(p, seed, offset, state))
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        state, = ctx.saved_tensors
-        return _drop(dy, B.dropout_key(*ctx.args, state)), None, None, None, None
+def _load():
+    """The host extension (autograd and marshalling), loaded once.  Raises
+    ImportError when it, or the library, has not been built."""
+    global _ext
+    if _ext is None:
+        B._load_rows()
+        if not os.path.exists(EXT_PATH):
+            raise ImportError(f"{EXT_PATH} is missing: build it with __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("fo_rows_torch", EXT_PATH)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.set_error(B.FoError)
+        _ext = ext
+    return _ext
 
 
 def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, state: torch.Tensor | None = None) -> torch.Tensor:
@@ -85,9 +59,7 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, state: torch.
     `state`: 2 int64 on the GPU added to (seed, offset) when the kernels run
     (see DropoutCounter); they may not be changed before the backward pass.
     Dropped elements are 0 even where x is NaN or infinite.  p = 0 returns x."""
-    if _check_p(p) == 0.0:
-        return x
-    return _Dropout.apply(x, float(p), seed, offset, state)
+    return (_ext or _load()).dropout(x, p, seed & _M64, offset & _M64, state)
 
 
 class DropoutCounter:
@@ -131,95 +103,26 @@ class DropoutCounter:
             self.state.copy_(torch.tensor(sd["state"], dtype=torch.int64))
 
 
-# ---------------------------------------------------------------------------
-# norms
-# ---------------------------------------------------------------------------
-def _norm_forward(x, residual, weight, bias, eps, kind, key, stats):
-    """(h or None, y, mean or None, rstd or None)."""
-    xr = _rows(x)
-    rows = xr.shape[0]
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = torch.empty_like(y) if residual is not None else None
-    mean = torch.empty(rows, dtype=torch.float32, device=x.device) if stats and kind == "layer" else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
-    B.fo_norm_forward(xr, y.view(xr.shape), kind, _flat(weight), _flat(bias), eps,
-                      None if residual is None else _rows(residual), None if h is None else h.view(xr.shape),
-                      mean, rstd, key)
-    return h, y, mean, rstd
+def _norm(x, residual, weight, bias, eps, kind, p=0.0, seed=0, offset=0, state=None):
+    return (_ext or _load()).norm(x, residual, weight, bias, eps, kind, p, seed & _M64, offset & _M64, state)
 
 
-class _Norm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, residual, weight, bias, eps, kind, p, seed, offset, state):
-        h, y, mean, rstd = _norm_forward(x, residual, weight, bias, eps, kind,
-                                         B.dropout_key(p, seed, offset, state) if p else None, True)
-        ctx.save_for_backward(x if h is None else h, weight, mean, rstd, state)
-        ctx.args = (kind, p, seed, offset, None if bias is None else bias.dtype)
-        ctx.set_materialize_grads(False)
-        return y if h is None else (h, y)
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, *grads):
-        h, weight, mean, rstd, state = ctx.saved_tensors
-        kind, p, seed, offset, bias_dtype = ctx.args
-        dy, dh = grads[-1], grads[0] if len(grads) == 2 else None
-        need_x, need_res, need_w, need_b = ctx.needs_input_grad[:4]
-        key = B.dropout_key(p, seed, offset, state) if p else None
-        rest = (None,) * 6
-        if dy is None:                              # only h was used: the norm has no part in it
-            if dh is None:
-                return (None,) * 10
-            dx = None if not need_x else _drop(dh, key) if key else dh
-            return (dx, dh if need_res else None, None, None) + rest
-
-        hr = _rows(h)
-
-        def like_h():
-            return torch.empty(h.shape, dtype=h.dtype, device=h.device)
-
-        # without dropout the gradients of x and of the residual are one tensor
-        d = like_h() if need_res or (need_x and not key) else None
-        dx = like_h() if need_x and key else None
-        dw = torch.empty(weight.shape, dtype=weight.dtype, device=h.device) if need_w else None
-        db = torch.empty(hr.shape[1], dtype=bias_dtype, device=h.device) if need_b else None
-        B.fo_norm_backward(_rows(dy), hr, rstd, kind, mean, _flat(weight), None if dh is None else _rows(dh),
-                           None if d is None else d.view(hr.shape), None if dx is None else dx.view(hr.shape),
-                           dw, db, drop=key)
-        if need_x and not key:
-            dx = d
-        return (dx, d if need_res else None, dw, db) + rest
-
-
-def _norm(x, residual, weight, bias, eps, kind, p, seed, offset, state):
-    p = _check_p(p)
-    if x.dim() == 0 or x.shape[-1] == 0:
-        raise ValueError(f"a norm needs a last dimension of at least one element, got shape {tuple(x.shape)}")
-    cols = x.shape[-1]
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None and t.shape != (cols,):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({cols},)")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError(f"weight is {weight.dtype} and bias {bias.dtype}: they must agree")
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
-        raise ValueError(f"the residual must be {tuple(x.shape)} of {x.dtype}, "
-                         f"got {tuple(residual.shape)} of {residual.dtype}")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, residual, weight, bias)):
-        return _Norm.apply(x, residual, weight, bias, float(eps), kind, p, seed, offset, state)
-    h, y, _, _ = _norm_forward(x, residual, weight, bias, eps, kind,
-                               B.dropout_key(p, seed, offset, state) if p else None, False)
-    return y if h is None else (h, y)
+def _join(x, residual, *args):
+    if residual is None:
+        raise ValueError("the fused form needs a residual")
+    h, y = _norm(x, residual, *args)
+    return h, y
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                eps: float = 1e-5) -> torch.Tensor:
     """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension."""
-    return _norm(x, None, weight, bias, eps, "layer", 0.0, 0, 0, None)
+    return _norm(x, None, weight, bias, eps, B.FO_LAYER_NORM)[0]
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6) -> torch.Tensor:
     """x / sqrt(mean(x^2) + eps) * weight over the last dimension."""
-    return _norm(x, None, weight, None, eps, "rms", 0.0, 0, 0, None)
+    return _norm(x, None, weight, None, eps, B.FO_RMS_NORM)[0]
 
 
 def dropout_add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor | None = None,
@@ -227,14 +130,14 @@ def dropout_add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torc
                            offset: int = 0, state: torch.Tensor | None = None):
     """(h, layer_norm(h)) with h = residual + dropout(x, p), in one pass each way.
     h is rounded to x's type, and the norm is that of the rounded h."""
-    return _norm(x, residual, weight, bias, eps, "layer", p, seed, offset, state)
+    return _join(x, residual, weight, bias, eps, B.FO_LAYER_NORM, p, seed, offset, state)
 
 
 def dropout_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor | None = None,
                          eps: float = 1e-6, *, p: float = 0.0, seed: int = 0, offset: int = 0,
                          state: torch.Tensor | None = None):
     """(h, rms_norm(h)) with h = residual + dropout(x, p)."""
-    return _norm(x, residual, weight, None, eps, "rms", p, seed, offset, state)
+    return _join(x, residual, weight, None, eps, B.FO_RMS_NORM, p, seed, offset, state)
 
 
 # ---------------------------------------------------------------------------
@@ -278,7 +181,9 @@ class FlashDropout(torch.nn.Module):
 
     def __init__(self, p: float, counter: DropoutCounter):
         super().__init__()
-        self.p, self.counter = _check_p(p), counter
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"the drop probability must lie in [0, 1], got {p}")
+        self.p, self.counter = float(p), counter
 
     def forward(self, x):
         if not self.training or self.p == 0.0:
