@@ -87,10 +87,88 @@ unsigned grid_of(int64_t want) { return (unsigned)std::max<int64_t>(1, std::min<
     else hipLaunchKernelGGL(KERNEL<F32>, __VA_ARGS__);                     \
   } while (0)
 
-// Row ranges the weight gradients are summed over before the ranges are added:
-// the same for a given matrix on every device, so the order of the sums is too.
-int param_splits(int64_t rows, int64_t cols) {
-  return (int)std::min<int64_t>((rows + 7) / 8, 256);
+// How a row is spread over lanes: `lanes` of them with `chunks` 8-element chunks
+// each, or lanes = 0 for rows that do not fit registers.  Two chunks per lane of
+// a 16-bit type (one of float32, the same bytes) keep a lane's share of the rows,
+// of the next rows, of the weight and of both weight gradients within 128
+// registers, the most that leaves 16 waves on a compute unit.
+struct Spread { int lanes, chunks; };
+
+Spread spread_of(int64_t cols, int dtype) {
+  const int64_t n = (cols + 7) / 8;
+  for (int lanes = 8; lanes <= 64; lanes *= 2)
+    if (n <= lanes) return {lanes, 1};
+  const int per = dtype == FO_F32 ? 1 : 2;
+  for (int lanes = 64; lanes <= 1024; lanes *= 2)
+    if (n <= (int64_t)lanes * per) return {lanes, per};
+  return {0, 0};
+}
+
+constexpr int fwd_threads(int lanes) { return std::max(lanes, 256); }
+constexpr int bwd_threads(int lanes) { return std::max(lanes, 512); }
+
+// Workgroups of the kernels that walk over the rows: enough to fill the 256
+// compute units a few times over, and for the backward pass no more, because
+// each writes a partial sum of every weight gradient.  Constants, so that the
+// order of those sums is the same on every device.
+constexpr int64_t kFwdGroups = 2048;
+constexpr int64_t kBwdGroups = 512;
+constexpr int kLongSplits = 256;
+
+int64_t bwd_splits(int64_t rows, int64_t cols, int dtype) {
+  const Spread s = spread_of(cols, dtype);
+  if (!s.lanes) return std::min<int64_t>((rows + 7) / 8, kLongSplits);
+  const int64_t at_a_time = bwd_threads(s.lanes) / s.lanes;
+  return std::min<int64_t>((rows + at_a_time - 1) / at_a_time, kBwdGroups);
+}
+
+template <typename T, int LANES, int NV, int MODE>
+void launch_fwd(const FwdArgs& a, hipStream_t s) {
+  constexpr int threads = fwd_threads(LANES);
+  const int64_t groups = (a.rows + threads / LANES - 1) / (threads / LANES);
+  hipLaunchKernelGGL((k_norm_fwd<T, LANES, NV, threads, MODE>), (unsigned)std::min(groups, kFwdGroups), threads, 0, s, a);
+}
+
+template <typename T, int LANES, int NV, int MODE>
+void launch_bwd(const BwdArgs& a, hipStream_t s) {
+  constexpr int threads = bwd_threads(LANES);
+  hipLaunchKernelGGL((k_norm_bwd<T, LANES, NV, threads, MODE>), (unsigned)a.splits, threads, 0, s, a);
+}
+
+template <typename T, int LANES, int NV>
+void launch_mode(int mode, const FwdArgs& a, hipStream_t s) {
+  if (mode == PLAIN) launch_fwd<T, LANES, NV, PLAIN>(a, s);
+  else if (mode == RESIDUAL) launch_fwd<T, LANES, NV, RESIDUAL>(a, s);
+  else launch_fwd<T, LANES, NV, DROPPED>(a, s);
+}
+template <typename T, int LANES, int NV>
+void launch_mode(int mode, const BwdArgs& a, hipStream_t s) {
+  if (mode == PLAIN) launch_bwd<T, LANES, NV, PLAIN>(a, s);
+  else if (mode == RESIDUAL) launch_bwd<T, LANES, NV, RESIDUAL>(a, s);
+  else launch_bwd<T, LANES, NV, DROPPED>(a, s);
+}
+
+template <typename T, typename Args>
+void launch_spread(Spread sp, int mode, const Args& a, hipStream_t s) {
+  constexpr int per = is_f32<T> ? 1 : 2;
+  switch (sp.lanes * 4 + sp.chunks) {
+    case 8 * 4 + 1: return launch_mode<T, 8, 1>(mode, a, s);
+    case 16 * 4 + 1: return launch_mode<T, 16, 1>(mode, a, s);
+    case 32 * 4 + 1: return launch_mode<T, 32, 1>(mode, a, s);
+    case 64 * 4 + 1: return launch_mode<T, 64, 1>(mode, a, s);
+    case 128 * 4 + per: return launch_mode<T, 128, per>(mode, a, s);
+    case 256 * 4 + per: return launch_mode<T, 256, per>(mode, a, s);
+    case 512 * 4 + per: return launch_mode<T, 512, per>(mode, a, s);
+    case 1024 * 4 + per: return launch_mode<T, 1024, per>(mode, a, s);
+  }
+  if constexpr (!is_f32<T>) return launch_mode<T, 64, 2>(mode, a, s);     // the one spread left
+}
+
+template <typename Args>
+void launch_rows(int dtype, Spread sp, int mode, const Args& a, hipStream_t s) {
+  if (dtype == FO_BF16) launch_spread<Bf16>(sp, mode, a, s);
+  else if (dtype == FO_FP16) launch_spread<Fp16>(sp, mode, a, s);
+  else launch_spread<F32>(sp, mode, a, s);
 }
 
 }  // namespace
@@ -150,7 +228,10 @@ int fo_norm_forward(const fo_norm_fwd* in, void* stream) {
   a.rows = rows; a.x_ld = in->x_ld; a.residual_ld = in->residual_ld;
   a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms;
   a.eps = (float)in->eps; a.inv_cols = (float)(1.0 / (double)cols);
-  FO_BY_TYPE(in->dtype, k_norm_fwd_long, grid_of(rows), BLOCK, 0, static_cast<hipStream_t>(stream), a);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Spread sp = spread_of(cols, in->dtype);
+  if (sp.lanes) launch_rows(in->dtype, sp, !in->residual ? PLAIN : a.dropping ? DROPPED : RESIDUAL, a, s);
+  else FO_BY_TYPE(in->dtype, k_norm_fwd_long, grid_of(rows), BLOCK, 0, s, a);
   return launch_check("norm forward launch");
 }
 
@@ -158,7 +239,9 @@ int fo_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
   clear_error();
   if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
   FO_TRY(shape_ok(rows, cols));
-  *bytes = 2 * (int64_t)param_splits(rows, cols) * cols * (int64_t)sizeof(float);
+  int64_t splits = 0;                          // of the element type that needs the most
+  for (int dtype : {(int)FO_BF16, (int)FO_FP16, (int)FO_F32}) splits = std::max(splits, bwd_splits(rows, cols, dtype));
+  *bytes = 2 * splits * cols * (int64_t)sizeof(float);
   return FO_OK;
 }
 
@@ -177,7 +260,7 @@ int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
   const int64_t rows = in->rows, cols = in->cols;
   const size_t es = elem_size(in->dtype), ws = elem_size(in->wdtype);
   const bool any = rows > 0, params = in->dweight || in->dbias, grads = in->d || in->dx;
-  const int splits = param_splits(rows, cols);
+  const int64_t splits = bwd_splits(rows, cols, in->dtype);
   Arrays ar;
   FO_TRY(ar.add(in->dy, "dy", false, any, rows, cols, in->dy_ld, es));
   FO_TRY(ar.add(in->dh, "dh", false, false, rows, cols, in->dh_ld, es));
@@ -190,7 +273,7 @@ int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
   FO_TRY(ar.add(in->dweight, "dweight", true, false, 1, cols, 0, ws));
   FO_TRY(ar.add(in->dbias, "dbias", true, false, 1, cols, 0, ws));
   if (params && any) {
-    const int64_t need = 2 * (int64_t)splits * cols * (int64_t)sizeof(float);
+    const int64_t need = 2 * splits * cols * (int64_t)sizeof(float);
     if (in->workspace_bytes < need)
       return fail(FO_EINVAL, "the workspace holds %lld bytes, %lld are needed", (long long)in->workspace_bytes,
                   (long long)need);
@@ -198,21 +281,24 @@ int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
   }
   FO_TRY(ar.disjoint());
   a.dy = in->dy; a.dh = in->dh; a.h = in->h; a.weight = in->weight; a.mean = in->mean; a.rstd = in->rstd;
-  a.d = in->d; a.dx = in->dx; a.partial = (float*)in->workspace;
+  a.d = in->d; a.dx = in->dx; a.partial = params ? (float*)in->workspace : nullptr;
   a.rows = rows; a.dy_ld = in->dy_ld; a.dh_ld = in->dh_ld; a.h_ld = in->h_ld;
-  a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms; a.splits = splits;
+  a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms; a.splits = (int)splits;
   a.inv_cols = (float)(1.0 / (double)cols);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (any && grads) {
-    FO_BY_TYPE(in->dtype, k_norm_bwd_rows_long, grid_of(rows), BLOCK, 0, s, a);
+  const Spread sp = spread_of(cols, in->dtype);
+  if (any && sp.lanes) {
+    if (grads || params)
+      launch_rows(in->dtype, sp, in->dx ? DROPPED : in->dh ? RESIDUAL : PLAIN, a, s);
+    FO_TRY(launch_check("norm backward launch"));
+  } else if (any) {
+    if (grads) FO_BY_TYPE(in->dtype, k_norm_bwd_rows_long, grid_of(rows), BLOCK, 0, s, a);
+    if (params)
+      FO_BY_TYPE(in->dtype, k_norm_bwd_cols_long, dim3((unsigned)((cols + 255) / 256), (unsigned)splits), BLOCK, 0, s, a);
     FO_TRY(launch_check("norm backward launch"));
   }
   if (params) {
-    if (any) {
-      FO_BY_TYPE(in->dtype, k_norm_bwd_cols_long, dim3((unsigned)((cols + 255) / 256), (unsigned)splits), BLOCK, 0, s, a);
-      FO_TRY(launch_check("weight gradient launch"));
-    }
-    ReduceArgs r = {(const float*)in->workspace, in->dweight, in->dbias, (int)cols, any ? splits : 0, in->wdtype};
+    ReduceArgs r = {(const float*)in->workspace, in->dweight, in->dbias, (int)cols, any ? (int)splits : 0, in->wdtype};
     hipLaunchKernelGGL(k_norm_bwd_reduce, dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, s, r);
     FO_TRY(launch_check("weight gradient sum launch"));
   }

@@ -123,6 +123,341 @@ __device__ __forceinline__ Chunk<T> join_chunk(const FwdArgs& a, const DropKey& 
   return to_chunk<T>(f);
 }
 
+// ---------------------------------------------------------------------------
+// sums over the lanes that share a row
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// lanes that differ in bits [log2 FROM, log2 TO) of their index end with the
+// same sum: register moves only (DPP inside 16 lanes, the gfx950 half swaps
+// beyond), 2 instructions per step where a shuffle through LDS takes a round
+// trip
+template <int FROM, int TO>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (FROM <= 1 && TO > 1) v = dpp_add<0xB1>(v);      // quad_perm [1,0,3,2]
+  if constexpr (FROM <= 2 && TO > 2) v = dpp_add<0x4E>(v);      // quad_perm [2,3,0,1]
+  if constexpr (FROM <= 4 && TO > 4) {
+    static_assert(FROM == 1, "the mirror below needs equal quads");
+    v = dpp_add<0x141>(v);                                      // row_half_mirror: the other quad of 8
+  }
+  if constexpr (FROM <= 8 && TO > 8) v = dpp_add<0x128>(v);     // row_ror:8
+  if constexpr (FROM <= 16 && TO > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (FROM <= 32 && TO > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// rows kept in registers
+// ---------------------------------------------------------------------------
+// LANES lanes share a row and hold NV chunks each: lane l the chunks l, l +
+// LANES, ...; a workgroup of THREADS works on THREADS / LANES rows at a time and
+// walks over the matrix, so that weights are loaded once per workgroup.  Loads
+// of the next rows are issued before the current ones are worked on.
+template <int LANES, int THREADS>
+struct Team {
+  static constexpr int ROWS = THREADS / LANES;               // at a time
+  static constexpr int WAVES = LANES > 64 ? LANES / 64 : 1;  // of one row
+};
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_or_zero(const typename T::raw* p, int cnt) {
+  if (cnt > 0) return load_chunk<T>(p, cnt);
+  Chunk<T> c;
+#pragma unroll
+  for (int i = 0; i < dwords<T>; ++i) c.w[i] = 0;
+  return c;
+}
+
+enum { PLAIN = 0, RESIDUAL = 1, DROPPED = 2 };
+
+// elements of a row that wave i of its team holds
+template <int LANES, int NV>
+__device__ __forceinline__ float team_count(int cols, int i) {
+  int n = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) n += max(0, min(512, cols - (i * 64 + v * LANES) * 8));
+  return (float)n;
+}
+
+template <typename T, int LANES, int NV, int THREADS, int MODE>
+__global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
+  typedef typename T::raw raw;
+  typedef Team<LANES, THREADS> G;
+  constexpr int W = G::WAVES;
+  __shared__ float red[2][G::ROWS][W][2];                    // of the waves of one row; used in turn
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
+  const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
+
+  int col[NV], cnt[NV];
+  float w[NV][8], b[NV][8], n = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    col[v] = (lane + v * LANES) * 8;
+    cnt[v] = a.cols - col[v];
+    if (cnt[v] > 0) {
+      load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, w[v]);
+      load_param(a.bias, a.wdtype, col[v], cnt[v], 0.0f, b[v]);
+      n += (float)min(cnt[v], 8);
+    }
+  }
+  // elements of this row that this wave holds, and of every other wave's
+  const float n_wave = lane_sum<1, (LANES < 64 ? LANES : 64)>(n);
+  const float inv_wave = n_wave > 0.0f ? 1.0f / n_wave : 0.0f;
+
+  auto fetch = [&](int64_t row, Chunk<T>* x, Chunk<T>* res) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = row < a.rows ? cnt[v] : 0;
+      x[v] = load_or_zero<T>((const raw*)a.x + row * a.x_ld + col[v], c);
+      if constexpr (MODE != PLAIN) res[v] = load_or_zero<T>((const raw*)a.residual + row * a.residual_ld + col[v], c);
+    }
+  };
+
+  int phase = 0;
+  const int64_t step = (int64_t)gridDim.x * G::ROWS;
+  int64_t row = (int64_t)blockIdx.x * G::ROWS + grp;
+  Chunk<T> nx[NV], nres[NV];
+  fetch(row, nx, nres);
+  for (int64_t first = (int64_t)blockIdx.x * G::ROWS; first < a.rows; first += step, row += step) {
+    Chunk<T> x[NV], res[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) { x[v] = nx[v]; if constexpr (MODE != PLAIN) res[v] = nres[v]; }
+    if (first + step < a.rows) fetch(row + step, nx, nres);
+    const bool live = row < a.rows;
+
+    float s = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if constexpr (MODE != PLAIN) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = elem<T>(x[v], j);
+        if constexpr (MODE == DROPPED) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= a.drop.scale;
+          if (a.drop.all) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+          } else {
+            drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(lane + v * LANES), f);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += elem<T>(res[v], j);
+        x[v] = to_chunk<T>(f);
+        if (live && cnt[v] > 0) store_chunk<T>((raw*)a.h + row * a.cols + col[v], x[v], cnt[v]);
+      }
+      // elements past the row's end are 0 in x; a NaN elsewhere stays in its row
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = elem<T>(x[v], j);
+        if (a.rms) q = fmaf(f, f, q);
+        else s += f;
+      }
+    }
+    float mean = 0.0f, var;
+    if (a.rms) {
+      var = lane_sum<1, (LANES < 64 ? LANES : 64)>(q);
+    } else {
+      // mean and squares about it, of the wave's own part of the row
+      mean = lane_sum<1, (LANES < 64 ? LANES : 64)>(s) * (W > 1 ? inv_wave : a.inv_cols);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = j < cnt[v] ? elem<T>(x[v], j) - mean : 0.0f;
+          q = fmaf(t, t, q);
+        }
+      var = lane_sum<1, (LANES < 64 ? LANES : 64)>(q);
+    }
+    if constexpr (W > 1) {
+      // the waves' parts joined: squares about the common mean are the squares
+      // about each wave's own plus count * (difference of the means)^2
+      if ((lane & 63) == 0) { red[phase][grp][wave][0] = mean; red[phase][grp][wave][1] = var; }
+      __syncthreads();
+      float total = 0.0f;
+      var = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        var += red[phase][grp][i][1];
+        if (!a.rms) total = fmaf(red[phase][grp][i][0], team_count<LANES, NV>(a.cols, i), total);
+      }
+      mean = total * a.inv_cols;
+      if (!a.rms) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float t = red[phase][grp][i][0] - mean;
+          var = fmaf(t * t, team_count<LANES, NV>(a.cols, i), var);
+        }
+      }
+      phase ^= 1;       // the next row's writes cannot meet this row's reads: a barrier lies between
+    }
+    const float rstd = 1.0f / sqrtf(var * a.inv_cols + a.eps);
+    if (live && lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (cnt[v] > 0) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = fmaf((elem<T>(x[v], j) - mean) * rstd, w[v][j], b[v][j]);
+          store_chunk<T>((raw*)a.y + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
+        }
+    }
+  }
+}
+
+// Gradients, weight gradients included: every lane adds up dy u and dy of its
+// own columns over the rows its team meets, the teams of a workgroup add theirs
+// through LDS at the end, and k_norm_bwd_reduce adds the workgroups'.
+template <typename T, int LANES, int NV, int THREADS, int MODE>
+__global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
+  typedef typename T::raw raw;
+  typedef Team<LANES, THREADS> G;
+  constexpr int W = G::WAVES;
+  __shared__ float red[2][G::ROWS][W][2];
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
+  const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
+
+  int col[NV], cnt[NV];
+  float w[NV][8], dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    col[v] = (lane + v * LANES) * 8;
+    cnt[v] = a.cols - col[v];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) { w[v][j] = 0.0f; dw[v][j] = 0.0f; db[v][j] = 0.0f; }
+    if (cnt[v] > 0) load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, w[v]);
+  }
+
+  struct Row { Chunk<T> h[NV], dy[NV], dh[NV]; float mean, rstd; };
+  auto fetch = [&](int64_t row, Row& r) {
+    const bool live = row < a.rows;
+    r.mean = live && !a.rms ? a.mean[row] : 0.0f;
+    r.rstd = live ? a.rstd[row] : 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = live ? cnt[v] : 0;
+      r.h[v] = load_or_zero<T>((const raw*)a.h + row * a.h_ld + col[v], c);
+      r.dy[v] = load_or_zero<T>((const raw*)a.dy + row * a.dy_ld + col[v], c);
+      if constexpr (MODE != PLAIN) r.dh[v] = load_or_zero<T>((const raw*)a.dh + row * a.dh_ld + col[v], a.dh ? c : 0);
+    }
+  };
+
+  int phase = 0;
+  const int64_t step = (int64_t)gridDim.x * G::ROWS;
+  int64_t row = (int64_t)blockIdx.x * G::ROWS + grp;
+  Row next;
+  fetch(row, next);
+  for (int64_t first = (int64_t)blockIdx.x * G::ROWS; first < a.rows; first += step, row += step) {
+    const Row cur = next;
+    if (first + step < a.rows) fetch(row + step, next);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // past the row's end dy and w are 0 and u is some finite number of a finite row
+        const float u = (elem<T>(cur.h[v], j) - cur.mean) * cur.rstd, dy = elem<T>(cur.dy[v], j), g = dy * w[v][j];
+        s1 += g;
+        s2 = fmaf(g, u, s2);
+        dw[v][j] = fmaf(dy, u, dw[v][j]);
+        db[v][j] += dy;
+      }
+    if (!(a.d || a.dx)) continue;                   // weight gradients alone
+    s1 = lane_sum<1, (LANES < 64 ? LANES : 64)>(s1);
+    s2 = lane_sum<1, (LANES < 64 ? LANES : 64)>(s2);
+    if constexpr (W > 1) {
+      if ((lane & 63) == 0) { red[phase][grp][wave][0] = s1; red[phase][grp][wave][1] = s2; }
+      __syncthreads();
+      s1 = s2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) { s1 += red[phase][grp][i][0]; s2 += red[phase][grp][i][1]; }
+      phase ^= 1;
+    }
+    s1 = a.rms ? 0.0f : s1 * a.inv_cols;
+    s2 *= a.inv_cols;
+    if (row >= a.rows) continue;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (cnt[v] <= 0) continue;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = (elem<T>(cur.h[v], j) - cur.mean) * cur.rstd;
+        f[j] = (fmaf(elem<T>(cur.dy[v], j), w[v][j], -s1) - u * s2) * cur.rstd;
+        if constexpr (MODE != PLAIN) f[j] += elem<T>(cur.dh[v], j);
+      }
+      if (a.d) store_chunk<T>((raw*)a.d + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
+      if constexpr (MODE == DROPPED) {
+        if (a.dx) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= a.drop.scale;
+          if (a.drop.all) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+          } else {
+            drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(lane + v * LANES), f);
+          }
+          store_chunk<T>((raw*)a.dx + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
+        }
+      }
+    }
+  }
+  if (!a.partial) return;
+
+  // the workgroup's sums: lanes of a wave that hold the same columns first
+  // (teams smaller than a wave), then the waves (or teams) through LDS
+  constexpr int SHARE = LANES < 64 ? LANES : 64;             // lanes of a wave with columns of their own
+  constexpr int PARTS = LANES < 64 ? THREADS / 64 : G::ROWS;
+  constexpr int COLS = (LANES < 64 ? LANES : LANES) * 8;      // columns of one v
+  if constexpr (PARTS == 1 && SHARE == 64) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < cnt[v]) {
+          a.partial[(int64_t)blockIdx.x * a.cols + col[v] + j] = dw[v][j];
+          a.partial[((int64_t)a.splits + blockIdx.x) * a.cols + col[v] + j] = db[v][j];
+        }
+  } else {
+    __shared__ float sum[PARTS][COLS];
+    const int part = LANES < 64 ? threadIdx.x / 64 : grp;
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float f = which ? db[v][j] : dw[v][j];
+          f = lane_sum<SHARE, 64>(f);
+          if (LANES >= 64 || (threadIdx.x & 63) < LANES) sum[part][lane * 8 + j] = f;
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < COLS; c += THREADS) {
+          float f = 0.0f;
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i) f += sum[i][c];
+          const int at = v * LANES * 8 + c;
+          if (at < a.cols) a.partial[((int64_t)which * a.splits + blockIdx.x) * a.cols + at] = f;
+        }
+      }
+  }
+}
+
 // One workgroup per row, the row read once per pass: rows of any length.
 template <typename T>
 __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
