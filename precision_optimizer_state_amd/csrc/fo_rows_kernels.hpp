@@ -34,7 +34,7 @@ struct FwdArgs {
   const void *x, *residual, *weight, *bias;
   void *h, *y;
   float *mean, *rstd;
-  int64_t rows, x_ld, residual_ld;
+  int64_t rows, first_row, x_ld, residual_ld;     // first_row: of this launch (k_norm_fwd)
   int cols, wdtype, rms, dropping;
   float eps, inv_cols;
   DropArgs drop;
@@ -46,7 +46,7 @@ struct BwdArgs {
   void *d, *dx;
   float* partial;              // [2][splits][cols]: dw, db
   int64_t rows, dy_ld, dh_ld, h_ld;
-  int cols, wdtype, rms, dropping, splits;
+  int cols, wdtype, rms, splits;
   float inv_cols;
   DropArgs drop;
 };
@@ -56,25 +56,48 @@ __device__ __forceinline__ int chunks_of(int cols) { return (cols + 7) >> 3; }
 // ---------------------------------------------------------------------------
 // dropout (the gradient is the same call on the output's gradient)
 // ---------------------------------------------------------------------------
-template <typename T>
+// A stream with ~20 integer and ~40 other instructions per 8 elements beside it,
+// so HBM bound.  Chunks lie one after another in memory (FLAT: packed rows of
+// whole chunks) or are found by one division, in 32 bits where the number of
+// chunks allows (Index).  Two chunks per thread, loaded before either is worked
+// on.
+constexpr int DROP_PER = 2;
+
+template <typename T, bool FLAT, typename Index>
 __global__ __launch_bounds__(BLOCK) void k_dropout(DropoutArgs a) {
+  typedef typename T::raw raw;
   const int nch = chunks_of(a.cols);
-  const int64_t total = a.rows * nch;
+  const Index total = (Index)(a.rows * nch);
   const DropKey key = drop_key(a.drop);
-  for (int64_t i = (int64_t)blockIdx.x * BLOCK + threadIdx.x; i < total; i += (int64_t)gridDim.x * BLOCK) {
-    const int64_t r = i / nch;
-    const int c0 = (int)(i - r * nch) * 8, cnt = a.cols - c0;
-    const Chunk<T> in = load_chunk<T>((const typename T::raw*)a.x + r * a.x_ld + c0, cnt);
-    float f[8];
+  const int64_t step = (int64_t)gridDim.x * (BLOCK * DROP_PER);
+  for (int64_t base = (int64_t)blockIdx.x * (BLOCK * DROP_PER) + threadIdx.x; base < (int64_t)total; base += step) {
+    Chunk<T> in[DROP_PER];
+    int64_t at[DROP_PER];
+    int cnt[DROP_PER];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = elem<T>(in, j) * a.drop.scale;
-    if (a.drop.all) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    } else {
-      drop_chunk(a.drop, key, (uint64_t)i, f);
+    for (int v = 0; v < DROP_PER; ++v) {
+      const int64_t i = base + v * BLOCK;
+      int64_t src = i * 8;
+      at[v] = src;
+      cnt[v] = i < (int64_t)total ? 8 : 0;
+      if constexpr (!FLAT) {
+        const Index r = (Index)i / (Index)nch;
+        const int c0 = (int)((Index)i - r * (Index)nch) * 8;
+        src = (int64_t)r * a.x_ld + c0;
+        at[v] = (int64_t)r * a.cols + c0;
+        if (cnt[v]) cnt[v] = a.cols - c0;
+      }
+      in[v] = load_or_zero<T>((const raw*)a.x + src, cnt[v]);
     }
-    store_chunk<T>((typename T::raw*)a.y + r * (int64_t)a.cols + c0, to_chunk<T>(f), cnt);
+#pragma unroll
+    for (int v = 0; v < DROP_PER; ++v) {
+      if (cnt[v] <= 0) continue;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = elem<T>(in[v], j);
+      drop_chunk(a.drop, key, (uint64_t)(base + v * BLOCK), f);
+      store_chunk<T>((raw*)a.y + at[v], to_chunk<T>(f), cnt[v]);
+    }
   }
 }
 
@@ -102,25 +125,21 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 // residual + dropout(x) of one chunk
 template <typename T>
-__device__ __forceinline__ Chunk<T> join_chunk(const FwdArgs& a, const DropKey& key, int64_t row, int c0, int cnt,
-                                               const Chunk<T>& x) {
-  const Chunk<T> res = load_chunk<T>((const typename T::raw*)a.residual + row * a.residual_ld + c0, cnt);
+__device__ __forceinline__ Chunk<T> join(const Chunk<T>& x, const Chunk<T>& residual, bool dropping, const DropArgs& d,
+                                         const DropKey& key, uint64_t index) {
   float f[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = elem<T>(x, j);
-  if (a.dropping) {
+  if (dropping) drop_chunk(d, key, index, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= a.drop.scale;
-    if (a.drop.all) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    } else {
-      drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(c0 >> 3), f);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] += elem<T>(res, j);
+  for (int j = 0; j < 8; ++j) f[j] += elem<T>(residual, j);
   return to_chunk<T>(f);
+}
+
+// 1 / sqrt(v) to one unit in the last place: the hardware estimate where v is
+// well inside the normal range (it takes subnormals for 0), else the IEEE form
+__device__ __forceinline__ float rsqrt_of(float v) {
+  return v > 0x1p-100f ? __builtin_amdgcn_rsqf(v) : 1.0f / sqrtf(v);
 }
 
 // ---------------------------------------------------------------------------
@@ -159,175 +178,133 @@ __device__ __forceinline__ float lane_sum(float v) {
 // rows kept in registers
 // ---------------------------------------------------------------------------
 // LANES lanes share a row and hold NV chunks each: lane l the chunks l, l +
-// LANES, ...; a workgroup of THREADS works on THREADS / LANES rows at a time and
-// walks over the matrix, so that weights are loaded once per workgroup.  Loads
-// of the next rows are issued before the current ones are worked on.
+// LANES, ...; a workgroup of THREADS works on THREADS / LANES rows at a time.
 template <int LANES, int THREADS>
 struct Team {
   static constexpr int ROWS = THREADS / LANES;               // at a time
   static constexpr int WAVES = LANES > 64 ? LANES / 64 : 1;  // of one row
+  static constexpr int SHARE = LANES < 64 ? LANES : 64;      // lanes of one wave that hold one row
 };
-
-template <typename T>
-__device__ __forceinline__ Chunk<T> load_or_zero(const typename T::raw* p, int cnt) {
-  if (cnt > 0) return load_chunk<T>(p, cnt);
-  Chunk<T> c;
-#pragma unroll
-  for (int i = 0; i < dwords<T>; ++i) c.w[i] = 0;
-  return c;
-}
 
 enum { PLAIN = 0, RESIDUAL = 1, DROPPED = 2 };
 
-// elements of a row that wave i of its team holds
-template <int LANES, int NV>
-__device__ __forceinline__ float team_count(int cols, int i) {
-  int n = 0;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) n += max(0, min(512, cols - (i * 64 + v * LANES) * 8));
-  return (float)n;
-}
-
-template <typename T, int LANES, int NV, int THREADS, int MODE>
+// Forward: one row per team, HBM bound.  Every load of the row goes out at once;
+// the statistics are two sums over registers (mean, then squares about it).  One
+// short-lived workgroup per few rows measured faster than workgroups that stay,
+// hold the weights and fetch ahead (8192 x 4096 bf16 RMS norm, 25.8 us at the
+// best grid against 24.9 us): few registers, so more waves and their loads in
+// flight.  SAME: weight and bias are of the rows' type and are loaded as they are
+// with the row; else they are widened after the sums (1-7% slower).
+template <typename T, int LANES, int NV, int THREADS, int MODE, bool SAME>
 __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
   typedef typename T::raw raw;
   typedef Team<LANES, THREADS> G;
   constexpr int W = G::WAVES;
-  __shared__ float red[2][G::ROWS][W][2];                    // of the waves of one row; used in turn
+  __shared__ float red[2][G::ROWS][W];
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
+  const int64_t row = a.first_row + (int64_t)blockIdx.x * G::ROWS + grp;
+  const bool live = row < a.rows;
   const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
 
   int col[NV], cnt[NV];
-  float w[NV][8], b[NV][8], n = 0.0f;
+  Chunk<T> x[NV], res[NV], w[NV], b[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     col[v] = (lane + v * LANES) * 8;
-    cnt[v] = a.cols - col[v];
-    if (cnt[v] > 0) {
-      load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, w[v]);
-      load_param(a.bias, a.wdtype, col[v], cnt[v], 0.0f, b[v]);
-      n += (float)min(cnt[v], 8);
+    cnt[v] = live ? a.cols - col[v] : 0;
+    x[v] = load_or_zero<T>((const raw*)a.x + row * a.x_ld + col[v], cnt[v]);
+    if constexpr (MODE != PLAIN) res[v] = load_or_zero<T>((const raw*)a.residual + row * a.residual_ld + col[v], cnt[v]);
+  }
+  if constexpr (SAME) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      w[v] = load_or_zero<T>((const raw*)a.weight + col[v], a.weight ? cnt[v] : 0);
+      b[v] = load_or_zero<T>((const raw*)a.bias + col[v], a.bias ? cnt[v] : 0);
     }
   }
-  // elements of this row that this wave holds, and of every other wave's
-  const float n_wave = lane_sum<1, (LANES < 64 ? LANES : 64)>(n);
-  const float inv_wave = n_wave > 0.0f ? 1.0f / n_wave : 0.0f;
 
-  auto fetch = [&](int64_t row, Chunk<T>* x, Chunk<T>* res) {
+  float s = 0.0f, q = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = row < a.rows ? cnt[v] : 0;
-      x[v] = load_or_zero<T>((const raw*)a.x + row * a.x_ld + col[v], c);
-      if constexpr (MODE != PLAIN) res[v] = load_or_zero<T>((const raw*)a.residual + row * a.residual_ld + col[v], c);
+  for (int v = 0; v < NV; ++v) {
+    if constexpr (MODE != PLAIN) {
+      x[v] = join<T>(x[v], res[v], MODE == DROPPED, a.drop, key,
+                     (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(lane + v * LANES));
+      if (cnt[v] > 0) store_chunk<T>((raw*)a.h + row * a.cols + col[v], x[v], cnt[v]);
     }
-  };
-
-  int phase = 0;
-  const int64_t step = (int64_t)gridDim.x * G::ROWS;
-  int64_t row = (int64_t)blockIdx.x * G::ROWS + grp;
-  Chunk<T> nx[NV], nres[NV];
-  fetch(row, nx, nres);
-  for (int64_t first = (int64_t)blockIdx.x * G::ROWS; first < a.rows; first += step, row += step) {
-    Chunk<T> x[NV], res[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) { x[v] = nx[v]; if constexpr (MODE != PLAIN) res[v] = nres[v]; }
-    if (first + step < a.rows) fetch(row + step, nx, nres);
-    const bool live = row < a.rows;
-
-    float s = 0.0f, q = 0.0f;
+    for (int j = 0; j < 8; ++j) {                  // 0 past the row's end
+      const float f = elem<T>(x[v], j);
+      if (a.rms) q = fmaf(f, f, q);
+      else s += f;
+    }
+  }
+  float mean = 0.0f;
+  if (!a.rms) {
+    s = lane_sum<1, G::SHARE>(s);
+    if constexpr (W > 1) {
+      if ((lane & 63) == 0) red[0][grp][wave] = s;
+      __syncthreads();
+      s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if constexpr (MODE != PLAIN) {
-        float f[8];
+      for (int i = 0; i < W; ++i) s += red[0][grp][i];
+    }
+    mean = s * a.inv_cols;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = elem<T>(x[v], j);
-        if constexpr (MODE == DROPPED) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] *= a.drop.scale;
-          if (a.drop.all) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-          } else {
-            drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(lane + v * LANES), f);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += elem<T>(res[v], j);
-        x[v] = to_chunk<T>(f);
-        if (live && cnt[v] > 0) store_chunk<T>((raw*)a.h + row * a.cols + col[v], x[v], cnt[v]);
-      }
-      // elements past the row's end are 0 in x; a NaN elsewhere stays in its row
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float f = elem<T>(x[v], j);
-        if (a.rms) q = fmaf(f, f, q);
-        else s += f;
+        const float t = j < cnt[v] ? elem<T>(x[v], j) - mean : 0.0f;
+        q = fmaf(t, t, q);
       }
-    }
-    float mean = 0.0f, var;
-    if (a.rms) {
-      var = lane_sum<1, (LANES < 64 ? LANES : 64)>(q);
+  }
+  q = lane_sum<1, G::SHARE>(q);
+  if constexpr (W > 1) {
+    if ((lane & 63) == 0) red[1][grp][wave] = q;
+    __syncthreads();
+    q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) q += red[1][grp][i];
+  }
+  const float rstd = rsqrt_of(q * a.inv_cols + a.eps);
+  if (live && lane == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (cnt[v] <= 0) continue;
+    float f[8], pw[8], pb[8];
+    if constexpr (SAME) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) { pw[j] = a.weight ? elem<T>(w[v], j) : 1.0f; pb[j] = elem<T>(b[v], j); }
     } else {
-      // mean and squares about it, of the wave's own part of the row
-      mean = lane_sum<1, (LANES < 64 ? LANES : 64)>(s) * (W > 1 ? inv_wave : a.inv_cols);
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = j < cnt[v] ? elem<T>(x[v], j) - mean : 0.0f;
-          q = fmaf(t, t, q);
-        }
-      var = lane_sum<1, (LANES < 64 ? LANES : 64)>(q);
+      load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, pw);
+      load_param(a.bias, a.wdtype, col[v], cnt[v], 0.0f, pb);
     }
-    if constexpr (W > 1) {
-      // the waves' parts joined: squares about the common mean are the squares
-      // about each wave's own plus count * (difference of the means)^2
-      if ((lane & 63) == 0) { red[phase][grp][wave][0] = mean; red[phase][grp][wave][1] = var; }
-      __syncthreads();
-      float total = 0.0f;
-      var = 0.0f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        var += red[phase][grp][i][1];
-        if (!a.rms) total = fmaf(red[phase][grp][i][0], team_count<LANES, NV>(a.cols, i), total);
-      }
-      mean = total * a.inv_cols;
-      if (!a.rms) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float t = red[phase][grp][i][0] - mean;
-          var = fmaf(t * t, team_count<LANES, NV>(a.cols, i), var);
-        }
-      }
-      phase ^= 1;       // the next row's writes cannot meet this row's reads: a barrier lies between
-    }
-    const float rstd = 1.0f / sqrtf(var * a.inv_cols + a.eps);
-    if (live && lane == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-    if (live) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (cnt[v] > 0) {
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = fmaf((elem<T>(x[v], j) - mean) * rstd, w[v][j], b[v][j]);
-          store_chunk<T>((raw*)a.y + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
-        }
-    }
+    for (int j = 0; j < 8; ++j) f[j] = fmaf((elem<T>(x[v], j) - mean) * rstd, pw[j], pb[j]);
+    store_chunk<T>((raw*)a.y + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
   }
 }
 
-// Gradients, weight gradients included: every lane adds up dy u and dy of its
-// own columns over the rows its team meets, the teams of a workgroup add theirs
-// through LDS at the end, and k_norm_bwd_reduce adds the workgroups'.
+// Backward, weight gradients included: workgroups walk over the matrix, every
+// lane adds up dy u and dy of its own columns over the rows its team meets, the
+// teams of a workgroup add theirs through LDS at the end, and k_norm_bwd_reduce
+// adds the workgroups'.  One pass over h, dy and dh, HBM bound.
+//
+// One chunk per lane and one workgroup of 16 waves on each compute unit: a second
+// chunk costs 24 registers and drops the waves to 8, and twice the workgroups
+// write twice the partial sums (8192 x 4096 bf16 RMS norm, sums included: 42.8 us;
+// two chunks per lane 53.0, 512 workgroups of half the size 52.3).  AHEAD: the
+// next rows' loads go out before the current ones are worked on (42.8 us against
+// 46.6); with two chunks per lane, the widest rows, registers do not allow it.
 template <typename T, int LANES, int NV, int THREADS, int MODE>
 __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   typedef typename T::raw raw;
   typedef Team<LANES, THREADS> G;
   constexpr int W = G::WAVES;
-  __shared__ float red[2][G::ROWS][W][2];
+  constexpr bool AHEAD = NV == 1;
+  __shared__ float red[2][G::ROWS][W][2];                    // used in turn, so one barrier per row is enough
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
   const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
 
@@ -360,10 +337,15 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   const int64_t step = (int64_t)gridDim.x * G::ROWS;
   int64_t row = (int64_t)blockIdx.x * G::ROWS + grp;
   Row next;
-  fetch(row, next);
+  if constexpr (AHEAD) fetch(row, next);
   for (int64_t first = (int64_t)blockIdx.x * G::ROWS; first < a.rows; first += step, row += step) {
-    const Row cur = next;
-    if (first + step < a.rows) fetch(row + step, next);
+    Row cur;
+    if constexpr (AHEAD) {
+      cur = next;
+      if (first + step < a.rows) fetch(row + step, next);
+    } else {
+      fetch(row, cur);
+    }
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -377,8 +359,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
         db[v][j] += dy;
       }
     if (!(a.d || a.dx)) continue;                   // weight gradients alone
-    s1 = lane_sum<1, (LANES < 64 ? LANES : 64)>(s1);
-    s2 = lane_sum<1, (LANES < 64 ? LANES : 64)>(s2);
+    s1 = lane_sum<1, G::SHARE>(s1);
+    s2 = lane_sum<1, G::SHARE>(s2);
     if constexpr (W > 1) {
       if ((lane & 63) == 0) { red[phase][grp][wave][0] = s1; red[phase][grp][wave][1] = s2; }
       __syncthreads();
@@ -403,14 +385,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
       if (a.d) store_chunk<T>((raw*)a.d + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
       if constexpr (MODE == DROPPED) {
         if (a.dx) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] *= a.drop.scale;
-          if (a.drop.all) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-          } else {
-            drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(lane + v * LANES), f);
-          }
+          drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(lane + v * LANES), f);
           store_chunk<T>((raw*)a.dx + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
         }
       }
@@ -420,10 +395,9 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
 
   // the workgroup's sums: lanes of a wave that hold the same columns first
   // (teams smaller than a wave), then the waves (or teams) through LDS
-  constexpr int SHARE = LANES < 64 ? LANES : 64;             // lanes of a wave with columns of their own
   constexpr int PARTS = LANES < 64 ? THREADS / 64 : G::ROWS;
-  constexpr int COLS = (LANES < 64 ? LANES : LANES) * 8;      // columns of one v
-  if constexpr (PARTS == 1 && SHARE == 64) {
+  constexpr int COLS = LANES * 8;                            // columns of one v
+  if constexpr (PARTS == 1) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -443,7 +417,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float f = which ? db[v][j] : dw[v][j];
-          f = lane_sum<SHARE, 64>(f);
+          f = lane_sum<G::SHARE, 64>(f);
           if (LANES >= 64 || (threadIdx.x & 63) < LANES) sum[part][lane * 8 + j] = f;
         }
         __syncthreads();
@@ -471,7 +445,8 @@ __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
       const int cnt = a.cols - c0;
       Chunk<T> c = load_chunk<T>((const raw*)a.x + row * a.x_ld + c0, cnt);
       if (a.residual) {
-        c = join_chunk<T>(a, key, row, c0, cnt, c);
+        const Chunk<T> res = load_chunk<T>((const raw*)a.residual + row * a.residual_ld + c0, cnt);
+        c = join<T>(c, res, a.dropping, a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(c0 >> 3));
         store_chunk<T>((raw*)a.h + row * a.cols + c0, c, cnt);
       }
 #pragma unroll
@@ -492,7 +467,7 @@ __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
       }
       var = block_sum<BLOCK>(q, red) * a.inv_cols;
     }
-    const float rstd = 1.0f / sqrtf(var + a.eps);
+    const float rstd = rsqrt_of(var + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -553,14 +528,7 @@ __global__ __launch_bounds__(BLOCK) void k_norm_bwd_rows_long(BwdArgs a) {
       }
       if (a.d) store_chunk<T>((raw*)a.d + row * a.cols + c0, to_chunk<T>(f), cnt);
       if (a.dx) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= a.drop.scale;
-        if (a.drop.all) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-        } else {
-          drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(c0 >> 3), f);
-        }
+        drop_chunk(a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(c0 >> 3), f);
         store_chunk<T>((raw*)a.dx + row * a.cols + c0, to_chunk<T>(f), cnt);
       }
     }

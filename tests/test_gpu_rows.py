@@ -201,6 +201,17 @@ def test_norm_of_rows_far_from_zero():
     run_norm("layer", 11, 5000, "f32", "f32", loc=-1500.0)
 
 
+def test_more_rows_than_one_launch_covers():
+    # 2^31 threads hold 2^28 rows of 8 columns; both ends and the seam against the oracle
+    rows, cols = (1 << 28) + 37, 8
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    with torch.no_grad():
+        y = nn.layer_norm(x)
+    for at in (0, (1 << 28) - 16, rows - 16):
+        check_forward(f"rows from {at}", y[at:at + 16], host(x[at:at + 16]), None, None, 1e-5, "layer")
+    del x, y
+
+
 def test_join_that_drops_everything():
     run_norm("layer", 7, 100, "bf16", "bf16", join=True, p=1.0)
 
