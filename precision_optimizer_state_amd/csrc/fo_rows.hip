@@ -129,11 +129,12 @@ constexpr int kBwdThreads = 1024;
 // one partial sum per weight gradient.  A constant, so that the order of those
 // sums is the same on every device.
 constexpr int64_t kBwdGroups = 256;
+constexpr int64_t kColGroups = 2048;        // of k_norm_bwd_cols_long, over columns and ranges of rows
 
 int64_t bwd_splits(int64_t rows, int64_t cols, int dtype) {
   const Spread s = bwd_spread(cols, dtype);
-  const int64_t at_a_time = s.lanes ? kBwdThreads / s.lanes : 8;
-  return std::min<int64_t>((rows + at_a_time - 1) / at_a_time, kBwdGroups);
+  if (s.lanes) return std::min<int64_t>((rows * s.lanes + kBwdThreads - 1) / kBwdThreads, kBwdGroups);
+  return std::min<int64_t>((rows + 7) / 8, std::max<int64_t>(kColGroups / ((cols + 255) / 256), 1));
 }
 
 template <typename T, int LANES, int NV, int MODE, bool SAME>

@@ -119,14 +119,41 @@ __device__ __forceinline__ void store_chunk(typename T::raw* ptr, const Chunk<T>
     }
 }
 
-// cnt <= 0: nothing is read
+// A chunk of a row that begins at column `col`, in two steps, so that the loads
+// of several arrays are all on their way before any result is touched (a lane
+// that gathers a short last chunk element by element waits for each array in
+// turn: 4096 x 4095 bf16 layer norm, 17.4 and 31.6 us forward and backward so,
+// against 12.6 and 19.6 at 4096 columns).  load_part reads the last chunk of a
+// row that is no multiple of 8 long as the row's last 8 elements; settle_part
+// moves its own elements down and clears the rest.  Rows of fewer than 8
+// elements are gathered.  Nothing outside the row is read; a chunk past its end
+// is 0.
 template <typename T>
-__device__ __forceinline__ Chunk<T> load_or_zero(const typename T::raw* p, int cnt) {
-  if (cnt > 0) return load_chunk<T>(p, cnt);
+__device__ __forceinline__ Chunk<T> load_part(const typename T::raw* row, int col, int cols) {
   Chunk<T> c;
+  if (cols < 8 && col < cols) return load_chunk<T>(row + col, cols - col);
+  if (col < cols) return load_chunk<T>(row + min(col, cols - 8), 8);
 #pragma unroll
   for (int i = 0; i < dwords<T>; ++i) c.w[i] = 0;
   return c;
+}
+
+template <typename T>
+__device__ __forceinline__ void settle_part(Chunk<T>& c, int col, int cols) {
+  const int k = col + 8 - cols;                    // elements of the chunk before
+  if (cols < 8 || k <= 0 || k >= 8) return;
+  constexpr int N = dwords<T>;
+#pragma unroll
+  for (int step = N / 2; step; step >>= 1)         // whole dwords
+    if (k & (is_f32<T> ? step : 2 * step)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) c.w[i] = i + step < N ? c.w[i + step] : 0;
+    }
+  if constexpr (!is_f32<T>)
+    if (k & 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) c.w[i] = c.w[i] >> 16 | (i + 1 < N ? c.w[i + 1] << 16 : 0);
+    }
 }
 
 // Norm weights and biases come in any of the three types, whatever the rows

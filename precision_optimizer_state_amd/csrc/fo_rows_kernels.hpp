@@ -73,25 +73,27 @@ __global__ __launch_bounds__(BLOCK) void k_dropout(DropoutArgs a) {
   for (int64_t base = (int64_t)blockIdx.x * (BLOCK * DROP_PER) + threadIdx.x; base < (int64_t)total; base += step) {
     Chunk<T> in[DROP_PER];
     int64_t at[DROP_PER];
-    int cnt[DROP_PER];
+    int col[DROP_PER], cnt[DROP_PER];
 #pragma unroll
     for (int v = 0; v < DROP_PER; ++v) {
       const int64_t i = base + v * BLOCK;
-      int64_t src = i * 8;
-      at[v] = src;
-      cnt[v] = i < (int64_t)total ? 8 : 0;
-      if constexpr (!FLAT) {
-        const Index r = (Index)i / (Index)nch;
-        const int c0 = (int)((Index)i - r * (Index)nch) * 8;
-        src = (int64_t)r * a.x_ld + c0;
-        at[v] = (int64_t)r * a.cols + c0;
-        if (cnt[v]) cnt[v] = a.cols - c0;
+      const bool live = i < (int64_t)total;
+      if constexpr (FLAT) {
+        at[v] = i * 8;
+        cnt[v] = live ? 8 : 0;
+        in[v] = load_part<T>((const raw*)a.x + at[v], 0, cnt[v]);
+      } else {
+        const Index r = live ? (Index)i / (Index)nch : 0;
+        col[v] = live ? (int)((Index)i - r * (Index)nch) * 8 : a.cols;
+        at[v] = (int64_t)r * a.cols + col[v];
+        cnt[v] = a.cols - col[v];
+        in[v] = load_part<T>((const raw*)a.x + (int64_t)r * a.x_ld, col[v], a.cols);
       }
-      in[v] = load_or_zero<T>((const raw*)a.x + src, cnt[v]);
     }
 #pragma unroll
     for (int v = 0; v < DROP_PER; ++v) {
       if (cnt[v] <= 0) continue;
+      if constexpr (!FLAT) settle_part<T>(in[v], col[v], a.cols);
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = elem<T>(in[v], j);
@@ -174,6 +176,13 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
+// Sum over the waves of one row: each wave has left its own sum in slot[wave]
+// before a barrier.  One LDS read and log2(W) register steps.
+template <int W>
+__device__ __forceinline__ float waves_sum(const float* slot) {
+  return lane_sum<1, W>(slot[threadIdx.x % W]);
+}
+
 // ---------------------------------------------------------------------------
 // rows kept in registers
 // ---------------------------------------------------------------------------
@@ -211,17 +220,28 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     col[v] = (lane + v * LANES) * 8;
-    cnt[v] = live ? a.cols - col[v] : 0;
-    x[v] = load_or_zero<T>((const raw*)a.x + row * a.x_ld + col[v], cnt[v]);
-    if constexpr (MODE != PLAIN) res[v] = load_or_zero<T>((const raw*)a.residual + row * a.residual_ld + col[v], cnt[v]);
+    if (!live) col[v] = max(col[v], a.cols);
+    cnt[v] = a.cols - col[v];
+    x[v] = load_part<T>((const raw*)a.x + row * a.x_ld, col[v], a.cols);
+    if constexpr (MODE != PLAIN) res[v] = load_part<T>((const raw*)a.residual + row * a.residual_ld, col[v], a.cols);
   }
   if constexpr (SAME) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      w[v] = load_or_zero<T>((const raw*)a.weight + col[v], a.weight ? cnt[v] : 0);
-      b[v] = load_or_zero<T>((const raw*)a.bias + col[v], a.bias ? cnt[v] : 0);
+      w[v] = load_part<T>((const raw*)a.weight, a.weight ? col[v] : a.cols, a.cols);
+      b[v] = load_part<T>((const raw*)a.bias, a.bias ? col[v] : a.cols, a.cols);
     }
   }
+  if (a.cols % 8)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      settle_part<T>(x[v], col[v], a.cols);
+      if constexpr (MODE != PLAIN) settle_part<T>(res[v], col[v], a.cols);
+      if constexpr (SAME) {
+        settle_part<T>(w[v], col[v], a.cols);
+        settle_part<T>(b[v], col[v], a.cols);
+      }
+    }
 
   float s = 0.0f, q = 0.0f;
 #pragma unroll
@@ -244,9 +264,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
     if constexpr (W > 1) {
       if ((lane & 63) == 0) red[0][grp][wave] = s;
       __syncthreads();
-      s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) s += red[0][grp][i];
+      s = waves_sum<W>(red[0][grp]);
     }
     mean = s * a.inv_cols;
 #pragma unroll
@@ -261,9 +279,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
   if constexpr (W > 1) {
     if ((lane & 63) == 0) red[1][grp][wave] = q;
     __syncthreads();
-    q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) q += red[1][grp][i];
+    q = waves_sum<W>(red[1][grp]);
   }
   const float rstd = rsqrt_of(q * a.inv_cols + a.eps);
   if (live && lane == 0) {
@@ -304,7 +320,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   typedef Team<LANES, THREADS> G;
   constexpr int W = G::WAVES;
   constexpr bool AHEAD = NV == 1;
-  __shared__ float red[2][G::ROWS][W][2];                    // used in turn, so one barrier per row is enough
+  __shared__ float red[2][2][G::ROWS][W];                    // used in turn, so one barrier per row is enough
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
   const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
 
@@ -316,7 +332,6 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
     cnt[v] = a.cols - col[v];
 #pragma unroll
     for (int j = 0; j < 8; ++j) { w[v][j] = 0.0f; dw[v][j] = 0.0f; db[v][j] = 0.0f; }
-    if (cnt[v] > 0) load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, w[v]);
   }
 
   struct Row { Chunk<T> h[NV], dy[NV], dh[NV]; float mean, rstd; };
@@ -326,11 +341,20 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
     r.rstd = live ? a.rstd[row] : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = live ? cnt[v] : 0;
-      r.h[v] = load_or_zero<T>((const raw*)a.h + row * a.h_ld + col[v], c);
-      r.dy[v] = load_or_zero<T>((const raw*)a.dy + row * a.dy_ld + col[v], c);
-      if constexpr (MODE != PLAIN) r.dh[v] = load_or_zero<T>((const raw*)a.dh + row * a.dh_ld + col[v], a.dh ? c : 0);
+      const int c = live ? col[v] : a.cols;
+      r.h[v] = load_part<T>((const raw*)a.h + row * a.h_ld, c, a.cols);
+      r.dy[v] = load_part<T>((const raw*)a.dy + row * a.dy_ld, c, a.cols);
+      if constexpr (MODE != PLAIN) r.dh[v] = load_part<T>((const raw*)a.dh + row * a.dh_ld, a.dh ? c : a.cols, a.cols);
     }
+  };
+  auto settle = [&](Row& r) {
+    if (a.cols % 8)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        settle_part<T>(r.h[v], col[v], a.cols);
+        settle_part<T>(r.dy[v], col[v], a.cols);
+        if constexpr (MODE != PLAIN) settle_part<T>(r.dh[v], col[v], a.cols);
+      }
   };
 
   int phase = 0;
@@ -338,6 +362,9 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   int64_t row = (int64_t)blockIdx.x * G::ROWS + grp;
   Row next;
   if constexpr (AHEAD) fetch(row, next);
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if (cnt[v] > 0) load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, w[v]);
   for (int64_t first = (int64_t)blockIdx.x * G::ROWS; first < a.rows; first += step, row += step) {
     Row cur;
     if constexpr (AHEAD) {
@@ -346,6 +373,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
     } else {
       fetch(row, cur);
     }
+    settle(cur);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -362,11 +390,10 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
     s1 = lane_sum<1, G::SHARE>(s1);
     s2 = lane_sum<1, G::SHARE>(s2);
     if constexpr (W > 1) {
-      if ((lane & 63) == 0) { red[phase][grp][wave][0] = s1; red[phase][grp][wave][1] = s2; }
+      if ((lane & 63) == 0) { red[phase][0][grp][wave] = s1; red[phase][1][grp][wave] = s2; }
       __syncthreads();
-      s1 = s2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) { s1 += red[phase][grp][i][0]; s2 += red[phase][grp][i][1]; }
+      s1 = waves_sum<W>(red[phase][0][grp]);
+      s2 = waves_sum<W>(red[phase][1][grp]);
       phase ^= 1;
     }
     s1 = a.rms ? 0.0f : s1 * a.inv_cols;
@@ -588,7 +615,16 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_reduce(ReduceArgs a) {
   const float* src = a.partial + (int64_t)blockIdx.y * a.splits * a.cols;
   float s = 0.0f;
   if (col < a.cols)
-    for (int i = grp; i < a.splits; i += 32) s += ((const FO_GLB float*)src)[(int64_t)i * a.cols + col];
+    for (int first = grp; first < a.splits; first += 32 * 8) {
+      float f[8];                                   // loads of one turn go out together
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = first + 32 * k;
+        f[k] = i < a.splits ? ((const FO_GLB float*)src)[(int64_t)i * a.cols + col] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += f[k];
+    }
   part[grp][lane] = s;
   __syncthreads();
 #pragma unroll
