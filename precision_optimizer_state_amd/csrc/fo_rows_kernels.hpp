@@ -397,7 +397,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
       phase ^= 1;
     }
     s1 = a.rms ? 0.0f : s1 * a.inv_cols;
-    s2 *= a.inv_cols;
+    s2 *= -a.inv_cols;
     if (row >= a.rows) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -406,8 +406,9 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float u = (elem<T>(cur.h[v], j) - cur.mean) * cur.rstd;
-        f[j] = (fmaf(elem<T>(cur.dy[v], j), w[v][j], -s1) - u * s2) * cur.rstd;
-        if constexpr (MODE != PLAIN) f[j] += elem<T>(cur.dh[v], j);
+        const float t = fmaf(u, s2, elem<T>(cur.dy[v], j) * w[v][j] - s1);
+        if constexpr (MODE != PLAIN) f[j] = fmaf(t, cur.rstd, elem<T>(cur.dh[v], j));
+        else f[j] = t * cur.rstd;
       }
       if (a.d) store_chunk<T>((raw*)a.d + row * a.cols + col[v], to_chunk<T>(f), cnt[v]);
       if constexpr (MODE == DROPPED) {

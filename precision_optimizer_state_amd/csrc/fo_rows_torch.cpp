@@ -113,14 +113,24 @@ struct Key {
   fo_dropout_key with(const Tensor& state) const {
     return {p, seed, offset, state.defined() ? reinterpret_cast<const uint64_t*>(state.data_ptr()) : nullptr};
   }
-  void save(AutogradContext* ctx) const {
-    ctx->saved_data["p"] = p;
-    ctx->saved_data["seed"] = static_cast<int64_t>(seed);
-    ctx->saved_data["offset"] = static_cast<int64_t>(offset);
+};
+
+// What a backward pass needs besides tensors, kept as one entry of the context.
+struct Saved : torch::CustomClassHolder {
+  Key key;
+  int32_t kind = 0;
+  at::ScalarType bias_dtype = at::ScalarType::Undefined;
+
+  static void put(AutogradContext* ctx, const Key& key, int32_t kind = 0,
+                  at::ScalarType bias_dtype = at::ScalarType::Undefined) {
+    auto s = c10::make_intrusive<Saved>();
+    s->key = key;
+    s->kind = kind;
+    s->bias_dtype = bias_dtype;
+    ctx->saved_data["args"] = at::IValue::make_capsule(std::move(s));
   }
-  static Key saved(AutogradContext* ctx) {
-    return {ctx->saved_data["p"].toDouble(), static_cast<uint64_t>(ctx->saved_data["seed"].toInt()),
-            static_cast<uint64_t>(ctx->saved_data["offset"].toInt())};
+  static c10::intrusive_ptr<Saved> get(AutogradContext* ctx) {
+    return c10::static_intrusive_pointer_cast<Saved>(ctx->saved_data["args"].toCapsule());
   }
 };
 
@@ -165,11 +175,11 @@ Tensor drop(const Tensor& x, const Key& key, const Tensor& state) {
 struct Dropout : torch::autograd::Function<Dropout> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const Key& key, const MaybeTensor& state) {
     ctx->save_for_backward({value(state)});
-    key.save(ctx);
+    Saved::put(ctx, key);
     return drop(x, key, value(state));
   }
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-    return once({drop(grads[0], Key::saved(ctx), ctx->get_saved_variables()[0]), Tensor(), Tensor()});
+    return once({drop(grads[0], Saved::get(ctx)->key, ctx->get_saved_variables()[0]), Tensor(), Tensor()});
   }
 };
 
@@ -187,7 +197,7 @@ Tensor dropout(const Tensor& x, double p, uint64_t seed, uint64_t offset, const 
 // norms
 // ---------------------------------------------------------------------------
 struct Forward {
-  Tensor h, y, mean, rstd;
+  Tensor h, y, stats;     // stats: rstd of every row, then (layer norm) the means
 };
 
 Forward norm_forward(const Tensor& x, const Tensor& residual, const Tensor& weight, const Tensor& bias, double eps,
@@ -200,11 +210,7 @@ Forward norm_forward(const Tensor& x, const Tensor& residual, const Tensor& weig
   Forward f;
   f.y = empty_like_shape(x);
   if (res) f.h = empty_like_shape(x);
-  if (stats) {
-    const auto opt = x.options().dtype(at::kFloat);
-    f.rstd = at::empty({r.rows}, opt);
-    if (kind == FO_LAYER_NORM) f.mean = at::empty({r.rows}, opt);
-  }
+  if (stats) f.stats = at::empty({kind == FO_LAYER_NORM ? 2 : 1, r.rows}, x.options().dtype(at::kFloat));
   fo_norm_fwd a = {};
   a.x = r.ptr;
   a.residual = res ? res->ptr : nullptr;
@@ -212,8 +218,8 @@ Forward norm_forward(const Tensor& x, const Tensor& residual, const Tensor& weig
   a.bias = address(b);
   a.h = address(f.h);
   a.y = f.y.data_ptr();
-  a.mean = static_cast<float*>(address(f.mean));
-  a.rstd = static_cast<float*>(address(f.rstd));
+  a.rstd = static_cast<float*>(address(f.stats));
+  a.mean = a.rstd && kind == FO_LAYER_NORM ? a.rstd + r.rows : nullptr;
   a.rows = r.rows;
   a.cols = r.cols;
   a.x_ld = r.ld;
@@ -233,10 +239,8 @@ struct Norm : torch::autograd::Function<Norm> {
                                const Key& key, const MaybeTensor& state) {
     Forward f = norm_forward(x, value(residual), value(weight), value(bias), eps, static_cast<int>(kind), key,
                              value(state), true);
-    ctx->save_for_backward({f.h.defined() ? f.h : x, value(weight), f.mean, f.rstd, value(state)});
-    key.save(ctx);
-    ctx->saved_data["kind"] = kind;
-    ctx->saved_data["bias_dtype"] = static_cast<int64_t>(bias ? bias->scalar_type() : at::ScalarType::Undefined);
+    ctx->save_for_backward({f.h.defined() ? f.h : x, value(weight), f.stats, value(state)});
+    Saved::put(ctx, key, static_cast<int32_t>(kind), bias ? bias->scalar_type() : at::ScalarType::Undefined);
     ctx->set_materialize_grads(false);
     if (f.h.defined()) return {f.h, f.y};
     return {f.y};
@@ -244,17 +248,17 @@ struct Norm : torch::autograd::Function<Norm> {
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
     const variable_list saved = ctx->get_saved_variables();
-    const Tensor &h = saved[0], &weight = saved[1], &mean = saved[2], &rstd = saved[3], &state = saved[4];
-    const Key key = Key::saved(ctx);
+    const Tensor &h = saved[0], &weight = saved[1], &stats = saved[2], &state = saved[3];
+    const auto args = Saved::get(ctx);
+    const Key& key = args->key;
     const bool join = grads.size() == 2;
     const Tensor dy = grads.back(), dh = join ? grads[0] : Tensor();
-    const auto bias_dtype = static_cast<at::ScalarType>(ctx->saved_data["bias_dtype"].toInt());
     // the inputs that were there, in the order of forward's arguments
     size_t input = 0;
     const bool need_x = ctx->needs_input_grad(input++);
     const bool need_res = join && ctx->needs_input_grad(input++);
     const bool need_w = weight.defined() && ctx->needs_input_grad(input++);
-    const bool need_b = bias_dtype != at::ScalarType::Undefined && ctx->needs_input_grad(input++);
+    const bool need_b = args->bias_dtype != at::ScalarType::Undefined && ctx->needs_input_grad(input++);
     variable_list out(8);
     if (!dy.defined()) {                    // only h was used: the norm has no part in it
       if (!dh.defined()) return out;
@@ -270,7 +274,7 @@ struct Norm : torch::autograd::Function<Norm> {
     if (need_res || (need_x && key.p == 0.0)) d = empty_like_shape(h);
     if (need_x && key.p != 0.0) dx = empty_like_shape(h);
     if (need_w) dw = empty_like_shape(weight);
-    if (need_b) db = at::empty({rh.cols}, h.options().dtype(bias_dtype));
+    if (need_b) db = at::empty({rh.cols}, h.options().dtype(args->bias_dtype));
     const Tensor w = packed(weight);
     const Tensor& param = w.defined() ? w : db;
     fo_norm_bwd a = {};
@@ -283,8 +287,8 @@ struct Norm : torch::autograd::Function<Norm> {
     a.dh = rdh ? rdh->ptr : nullptr;
     a.h = rh.ptr;
     a.weight = address(w);
-    a.mean = static_cast<const float*>(address(mean));
-    a.rstd = static_cast<const float*>(address(rstd));
+    a.rstd = static_cast<const float*>(address(stats));
+    a.mean = a.rstd && args->kind == FO_LAYER_NORM ? a.rstd + rh.rows : nullptr;
     a.d = address(d);
     a.dx = address(dx);
     a.dweight = address(dw);
@@ -297,7 +301,7 @@ struct Norm : torch::autograd::Function<Norm> {
     a.drop = key.with(state);
     a.dtype = dtype_of(h);
     a.wdtype = param.defined() ? dtype_of(param) : a.dtype;
-    a.kind = static_cast<int32_t>(ctx->saved_data["kind"].toInt());
+    a.kind = args->kind;
     check(fo_norm_backward(&a, current_stream()));
     if (need_x) out[0] = key.p != 0.0 ? dx : d;
     if (need_res) out[1] = d;
