@@ -193,6 +193,12 @@ struct Team {
   static constexpr int ROWS = THREADS / LANES;               // at a time
   static constexpr int WAVES = LANES > 64 ? LANES / 64 : 1;  // of one row
   static constexpr int SHARE = LANES < 64 ? LANES : 64;      // lanes of one wave that hold one row
+  // which of the rows: the same for a whole wave where it can be, and then in
+  // scalar registers, as are the row's addresses
+  static __device__ __forceinline__ int index() {
+    const int i = threadIdx.x / LANES;
+    return LANES >= 64 ? __builtin_amdgcn_readfirstlane(i) : i;
+  }
 };
 
 enum { PLAIN = 0, RESIDUAL = 1, DROPPED = 2 };
@@ -210,7 +216,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
   typedef Team<LANES, THREADS> G;
   constexpr int W = G::WAVES;
   __shared__ float red[2][G::ROWS][W];
-  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
+  const int lane = threadIdx.x % LANES, grp = G::index(), wave = lane / 64;
   const int64_t row = a.first_row + (int64_t)blockIdx.x * G::ROWS + grp;
   const bool live = row < a.rows;
   const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
@@ -321,7 +327,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   constexpr int W = G::WAVES;
   constexpr bool AHEAD = NV == 1;
   __shared__ float red[2][2][G::ROWS][W];                    // used in turn, so one barrier per row is enough
-  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = lane / 64;
+  const int lane = threadIdx.x % LANES, grp = G::index(), wave = lane / 64;
   const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
 
   int col[NV], cnt[NV];
@@ -426,14 +432,13 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   constexpr int PARTS = LANES < 64 ? THREADS / 64 : G::ROWS;
   constexpr int COLS = LANES * 8;                            // columns of one v
   if constexpr (PARTS == 1) {
+    float* out = a.partial + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cnt[v]) {
-          a.partial[(int64_t)blockIdx.x * a.cols + col[v] + j] = dw[v][j];
-          a.partial[((int64_t)a.splits + blockIdx.x) * a.cols + col[v] + j] = db[v][j];
-        }
+      if (cnt[v] > 0) {
+        store_chunk<F32>(out + col[v], to_chunk<F32>(dw[v]), cnt[v]);
+        store_chunk<F32>(out + (int64_t)a.splits * a.cols + col[v], to_chunk<F32>(db[v]), cnt[v]);
+      }
   } else {
     __shared__ float sum[PARTS][COLS];
     const int part = LANES < 64 ? threadIdx.x / 64 : grp;
