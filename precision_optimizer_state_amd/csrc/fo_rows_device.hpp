@@ -107,7 +107,8 @@ __device__ __forceinline__ void store_chunk(typename T::raw* ptr, const Chunk<T>
 #pragma unroll
     for (int q = 0; q < dwords<T> / 4; ++q) {
       const v4u v = {c.w[4 * q], c.w[4 * q + 1], c.w[4 * q + 2], c.w[4 * q + 3]};
-      __builtin_nontemporal_store(v, (FO_GLB typename T::vec*)p + q);
+      if constexpr (is_f32<T>) ((FO_GLB typename T::vec*)p)[q] = v;
+      else __builtin_nontemporal_store(v, (FO_GLB typename T::vec*)p + q);
     }
     return;
   }
