@@ -97,9 +97,12 @@ __device__ __forceinline__ Chunk<T> load_chunk(const typename T::raw* ptr, int c
   return c;
 }
 
-// Stores carry the nontemporal hint: nothing here is read back by the kernel
-// that writes it.  Measured on an RMS norm of 8192 x 4096 bf16: 24.9 -> 20.0 us
-// (the time of a plain copy); the hint on the loads as well took it to 24.4.
+// Stores of 16-bit chunks carry the nontemporal hint: nothing here is read back
+// by the kernel that writes it.  Measured on an RMS norm of 8192 x 4096 bf16:
+// 24.9 -> 20.0 us (the time of a plain copy); the hint on the loads as well took
+// it to 24.4.  A float32 chunk is two stores 32 bytes apart from the next lane's,
+// which a plain store joins in cache: layer norm backward 32768 x 2048, 150 us
+// against 160 with the hint.
 template <typename T>
 __device__ __forceinline__ void store_chunk(typename T::raw* ptr, const Chunk<T>& c, int cnt) {
   FO_GLB typename T::raw* p = (FO_GLB typename T::raw*)ptr;
