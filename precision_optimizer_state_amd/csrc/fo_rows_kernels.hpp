@@ -325,7 +325,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   typedef typename T::raw raw;
   typedef Team<LANES, THREADS> G;
   constexpr int W = G::WAVES;
-  constexpr bool AHEAD = NV == 1, DEEP = AHEAD && !is_f32<T>;
+  constexpr bool AHEAD = NV == 1;
   __shared__ float red[2][2][G::ROWS][W];                    // used in turn, so one barrier per row is enough
   const int lane = threadIdx.x % LANES, grp = G::index(), wave = lane / 64;
   const DropKey key = MODE == DROPPED ? drop_key(a.drop) : DropKey{};
@@ -366,9 +366,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   int phase = 0;
   const int64_t step = (int64_t)gridDim.x * G::ROWS;
   int64_t row = (int64_t)blockIdx.x * G::ROWS + grp;
-  Row next, after;
+  Row next;
   if constexpr (AHEAD) fetch(row, next);
-  if constexpr (DEEP) fetch(row + step, after);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
     if (cnt[v] > 0) load_param(a.weight, a.wdtype, col[v], cnt[v], 1.0f, w[v]);
@@ -376,12 +375,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
     Row cur;
     if constexpr (AHEAD) {
       cur = next;
-      if constexpr (DEEP) {
-        next = after;
-        if (first + 2 * step < a.rows) fetch(row + 2 * step, after);
-      } else if (first + step < a.rows) {
-        fetch(row + step, next);
-      }
+      if (first + step < a.rows) fetch(row + step, next);
     } else {
       fetch(row, cur);
     }
