@@ -349,13 +349,15 @@ def _addr(t) -> c_void_p:
 
 def dropout_key(p, seed, offset=0, state=None) -> DropoutKey:
     """The key of a dropout mask: drop probability, 64-bit seed and offset, and
-    optionally 2 int64 of device memory added to them when the kernel runs."""
+    optionally 2 int64 of device memory added to them when the kernel runs
+    (the key keeps that tensor alive)."""
     if state is not None:
         import torch
         if state.dtype != torch.int64 or state.numel() != 2:
             raise ValueError("the dropout state must hold 2 int64")
-        state = _ptr(state).value
-    return DropoutKey(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1), state)
+    key = DropoutKey(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1), _ptr(state).value)
+    key._state = state
+    return key
 
 
 _NO_DROPOUT = DropoutKey(0.0, 0, 0, None)

@@ -16,7 +16,7 @@ using namespace fo::rows;
 
 namespace {
 
-constexpr int64_t kMaxCols = int64_t(1) << 30;     // a column index plus one launch step stays in 32 bits
+constexpr int64_t kMaxCols = int64_t(1) << 26;     // k_norm_bwd_reduce takes 32 threads per column
 constexpr int64_t kMaxRows = int64_t(1) << 40;
 constexpr int64_t kMaxThreads = int64_t(1) << 31;  // of one launch (a grid's threads must fit 32 bits)
 
@@ -25,7 +25,7 @@ bool dtype_ok(int dtype) { return dtype == FO_BF16 || dtype == FO_FP16 || dtype 
 
 int shape_ok(int64_t rows, int64_t cols) {
   if (rows < 0 || rows > kMaxRows) return fail(FO_EINVAL, "rows = %lld is not in [0, 2^40]", (long long)rows);
-  if (cols < 1 || cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^30]", (long long)cols);
+  if (cols < 1 || cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^26]", (long long)cols);
   return FO_OK;
 }
 

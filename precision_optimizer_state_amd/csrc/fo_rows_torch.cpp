@@ -6,6 +6,7 @@
 // pass through a Python autograd.Function took 140-230 us of host time, whatever
 // the size.
 #include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
@@ -63,6 +64,22 @@ void check_device(const Tensor& t) {
 }
 
 void* current_stream() { return c10::hip::getCurrentHIPStream().stream(); }
+
+// Under capture, the gradient of an input whose place in the autograd graph was
+// made on the default stream (a leaf that an eager graph, still alive, has used
+// too) would make that stream wait for the capturing one.  The runtime forbids
+// it, and the autograd engine ends the process when it happens in the captured
+// backward pass, so the forward call is refused.
+void check_capture(std::initializer_list<const Tensor*> inputs) {
+  if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
+  for (const Tensor* t : inputs) {
+    if (!t->defined() || !t->requires_grad()) continue;
+    const auto made_on = torch::autograd::impl::gradient_edge(*t).function->stream();
+    TORCH_CHECK(!made_on || made_on->id() != 0,
+                "this call is captured into a graph, but an input's gradient belongs to an autograd graph made on the "
+                "default stream: release that graph first, or capture with inputs detached from it");
+  }
+}
 
 // A tensor as a matrix: cols its last dimension, rows everything before.  The
 // tensor's own memory where its rows are consecutive elements at a constant
@@ -189,7 +206,10 @@ Tensor dropout(const Tensor& x, double p, uint64_t seed, uint64_t offset, const 
   if (p == 0.0) return x;
   check_device(x);
   dtype_of(x);
-  if (at::GradMode::is_enabled() && x.requires_grad()) return Dropout::apply(x, key, state);
+  if (at::GradMode::is_enabled() && x.requires_grad()) {
+    check_capture({&x});
+    return Dropout::apply(x, key, state);
+  }
   return drop(x, key, value(state));
 }
 
@@ -341,8 +361,10 @@ variable_list norm(const Tensor& x, const MaybeTensor& residual_arg, const Maybe
     check_device(residual);
     grad |= residual.requires_grad();
   }
-  if (grad && at::GradMode::is_enabled())
+  if (grad && at::GradMode::is_enabled()) {
+    check_capture({&x, &residual, &weight, &bias});
     return Norm::apply(x, residual_arg, weight_arg, bias_arg, eps, static_cast<int64_t>(kind), key, state_arg);
+  }
   Forward f = norm_forward(x, residual, weight, bias, eps, kind, key, state, false);
   if (f.h.defined()) return {f.h, f.y};
   return {f.y};

@@ -17,8 +17,10 @@ fo_norm_backward in include/foamd.h, which defines the formulas and the mask);
 a host extension (csrc/fo_rows_torch.cpp) marshals tensors and records the
 autograd graph.  Tensors must live
 on the current GPU; calls go to torch's current stream, allocate only through
-torch and never synchronise, so they can be captured into HIP graphs.  Norms
-are over the last dimension.  Inputs whose rows are not consecutive elements at
+torch and never synchronise, so they can be captured into HIP graphs (a captured
+call refuses leaves that an eager autograd graph, still alive, has used on the
+default stream: capture with detached leaves).  Norms are over the last
+dimension.  Inputs whose rows are not consecutive elements at
 a constant distance are copied first.  Gradients of gradients are not provided.
 """
 
@@ -59,7 +61,7 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, state: torch.
     `state`: 2 int64 on the GPU added to (seed, offset) when the kernels run
     (see DropoutCounter); they may not be changed before the backward pass.
     Dropped elements are 0 even where x is NaN or infinite.  p = 0 returns x."""
-    return (_ext or _load()).dropout(x, p, seed & _M64, offset & _M64, state)
+    return (_ext or _load()).dropout(x, p, int(seed) & _M64, int(offset) & _M64, state)
 
 
 class DropoutCounter:
@@ -104,7 +106,7 @@ class DropoutCounter:
 
 
 def _norm(x, residual, weight, bias, eps, kind, p=0.0, seed=0, offset=0, state=None):
-    return (_ext or _load()).norm(x, residual, weight, bias, eps, kind, p, seed & _M64, offset & _M64, state)
+    return (_ext or _load()).norm(x, residual, weight, bias, eps, kind, p, int(seed) & _M64, int(offset) & _M64, state)
 
 
 def _join(x, residual, *args):

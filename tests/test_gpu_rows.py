@@ -110,6 +110,17 @@ def test_dropout_past_32_bits():
     del x, y
 
 
+def test_dropout_of_more_chunks_than_one_launch_covers():
+    # 2^32 chunks of one element each and some more: the grid covers 2^32 chunks and loops for the rest
+    rows = (1 << 32) + 601
+    x = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    y = nn.dropout(x, 0.3, SEED, OFFSET)
+    for first in (0, (1 << 31) - 300, (1 << 32) - 300, rows - 600):
+        got = (y[first:first + 600] != 0).cpu().numpy()
+        assert np.array_equal(got, R.keep(600, 1, 0.3, SEED, OFFSET, first)), first
+    del x, y
+
+
 # ---------------------------------------------------------------------------
 # norms
 # ---------------------------------------------------------------------------
@@ -210,6 +221,11 @@ def test_more_rows_than_one_launch_covers():
     for at in (0, (1 << 28) - 16, rows - 16):
         check_forward(f"rows from {at}", y[at:at + 16], host(x[at:at + 16]), None, None, 1e-5, "layer")
     del x, y
+
+
+def test_very_long_rows():
+    run_norm("layer", 2, 3_000_017, "bf16", "f32", join=True, p=0.1)
+    run_norm("rms", 3, 1_000_000, "f32", "bf16")
 
 
 def test_join_that_drops_everything():
@@ -466,6 +482,26 @@ def test_two_graphs_do_not_share_a_workspace():
         torch.cuda.synchronize()
         for m in made:
             assert torch.equal(m[1], m[2])
+
+
+def test_capture_refuses_leaves_of_a_living_eager_graph():
+    x = torch.randn(8, 32, device="cuda", requires_grad=True)
+    w = torch.ones(32, device="cuda", requires_grad=True)
+    alive = nn.rms_norm(x, w)                        # made on the default stream, still alive
+    torch.cuda.synchronize()
+    for call in (lambda: nn.rms_norm(x, w), lambda: nn.dropout(x, 0.5, 1),
+                 lambda: nn.dropout_add_layer_norm(x.detach(), x.detach(), w)):
+        with pytest.raises(RuntimeError, match="default stream"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                call()
+    del alive
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                    # the eager graph is gone
+        y = nn.rms_norm(x, w)
+        gx, gw = torch.autograd.grad(y, [x, w], y.detach())
+    graph.replay()
+    torch.cuda.synchronize()
+    check_backward("captured", {"d": gx, "dweight": gw}, host(y), host(x), host(w), 1e-6, "rms")
 
 
 def test_state_changed_before_the_backward_pass_is_refused():

@@ -50,12 +50,12 @@ def test_struct_layouts():
     (dict(x=BASE + 1), B.FO_EINVAL, "aligned"),
     (dict(x=BASE + 2, dtype=B.FO_F32), B.FO_EINVAL, "aligned"),
     (dict(cols=0), B.FO_EINVAL, "cols"),
-    (dict(cols=(1 << 30) + 1), B.FO_EINVAL, "cols"),
+    (dict(cols=(1 << 26) + 1, x_ld=1 << 27), B.FO_EINVAL, "cols"),
     (dict(rows=-1), B.FO_EINVAL, "rows"),
     (dict(rows=(1 << 40) + 1), B.FO_EINVAL, "rows"),
     (dict(x_ld=-1), B.FO_EINVAL, "stride"),
     (dict(x_ld=(1 << 62)), B.FO_EINVAL, "address space"),
-    (dict(rows=1 << 40, cols=1 << 30, x_ld=0), B.FO_EINVAL, "address space"),
+    (dict(rows=1 << 40, cols=1 << 26, x_ld=0), B.FO_EINVAL, "address space"),
     (dict(dtype=3), B.FO_EINVAL, "element type"),
     (dict(wdtype=-1), B.FO_EINVAL, "element type"),
     (dict(kind=2), B.FO_EINVAL, "kind"),
