@@ -1,6 +1,10 @@
 /*
  * foamd.h -- C ABI of the MI355X (gfx950) fused low-precision optimizer step.
  *
+ * Below the optimizer step the header declares the row operators of a training
+ * step (dropout, layer norm, RMS norm and their fused form), which follow their
+ * usual textbook definitions.
+ *
  * The library implements the optimizer step described on the FlashOptim
  * pages: parameters held as a 16-bit downcast weight theta' plus an N-bit
  * ULP-normalised error-correction code (ECC), optimizer states held as
@@ -430,7 +434,8 @@ typedef struct fo_norm_fwd {
  *   h = residual + dropout(x), rounded to dtype (h = x without a residual)
  *   m = mean(h) (RMS norm: 0);  r = 1 / sqrt(mean((h - m)^2) + eps)
  *   y = (h - m) * r * weight + bias
- * The statistics are taken of the rounded h, from its values less their mean.
+ * The statistics are taken of the rounded h, from its values less their mean;
+ * rows whose squares overflow float32 (values past 1.8e19) get r = 0.
  * rows == 0 is a no-op.  Errors: FO_EINVAL, FO_EALIAS, FO_EHIP.
  */
 int fo_norm_forward(const fo_norm_fwd* args, void* stream);

@@ -2,9 +2,8 @@
 ULP-normalised error-correction code, companded 8-bit optimizer states, fused
 AdamW / Adam and momentum SGD over tensor lists; and the row operators of a
 training step around it (dropout, layer norm, RMS norm and their fused form,
-nn.py).  The compute lives in the HIP
-library csrc/ -> lib/libfoamd.so; binding.py marshals torch tensors into its
-C ABI (include/foamd.h)."""
+nn.py).  The compute lives in the HIP library csrc/ -> lib/libfoamd.so;
+binding.py marshals torch tensors into its C ABI (include/foamd.h)."""
 
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401

@@ -255,7 +255,7 @@ int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
   }
   if (params) {
     ReduceArgs r = {(const float*)in->workspace, in->dweight, in->dbias, (int)cols, any ? (int)splits : 0, in->wdtype};
-    hipLaunchKernelGGL(k_norm_bwd_reduce, dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, s, r);
+    hipLaunchKernelGGL(k_norm_bwd_reduce, dim3((unsigned)((cols + 31) / 32), in->dbias ? 2 : 1), 1024, 0, s, r);
     FO_TRY(launch_check("weight gradient sum launch"));
   }
   return FO_OK;

@@ -402,6 +402,65 @@ def test_on_a_side_stream():
     check_backward("side", {"dx": g}, host(r), host(want[0]), None, 1e-5, "layer", host(r), (0.1, 4, 0))
 
 
+def test_two_streams_at_once():
+    """Backward passes with weight gradients on two streams, unordered: each has its
+    own workspace, so both give what they give alone."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    data = [[torch.randn(4000, 1024, device="cuda", generator=gen) for _ in range(2)] for _ in range(2)]
+    w = torch.ones(1024, device="cuda", requires_grad=True)
+    alone = [torch.autograd.grad(nn.layer_norm(h, w), w, dy)[0] for h, dy in data]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for stream, (h, dy) in zip(streams, data):
+            with torch.cuda.stream(stream):
+                leaf = w.detach().requires_grad_(True)
+                got.append(torch.autograd.grad(nn.layer_norm(h, leaf), leaf, dy)[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, alone))
+
+
+def test_one_tensor_as_both_inputs_and_backward_twice():
+    x = torch.randn(30, 200, device="cuda", requires_grad=True)
+    dh, dy = torch.randn(30, 200, device="cuda"), torch.randn(30, 200, device="cuda")
+    h, y = nn.dropout_add_rms_norm(x, x, p=0.3, seed=np.int64(6))
+    first, = torch.autograd.grad([h, y], x, [dh, dy], retain_graph=True)
+    again, = torch.autograd.grad([h, y], x, [dh, dy])
+    assert torch.equal(first, again)
+    d, _, _ = R.norm_backward(host(dy), host(h), None, 1e-6, "rms", host(dh))
+    want = d + np.where(R.keep(30, 200, 0.3, 6, 0), d * R.scale(0.3), 0.0)
+    # two gradients within the bound of check_backward, below 2^-15 of values of order 1, and one sum
+    np.testing.assert_allclose(host(first), want, rtol=2.0 ** -15, atol=2.0 ** -15)
+    with pytest.raises(RuntimeError, match="second time"):
+        torch.autograd.grad([h, y], x, [dh, dy])
+
+
+def test_an_output_changed_before_the_backward_pass_is_refused():
+    x, r = (torch.randn(4, 16, device="cuda", requires_grad=True) for _ in range(2))
+    h, y = nn.dropout_add_layer_norm(x, r)
+    with torch.no_grad():
+        h.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_checkpointed_recomputation_finds_the_same_mask():
+    from torch.utils.checkpoint import checkpoint
+    counter = nn.DropoutCounter(seed=4)
+    x, r = (torch.randn(16, 64, device="cuda", requires_grad=True) for _ in range(2))
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    key = counter.next()
+
+    def block(x, r):
+        h, y = nn.dropout_add_rms_norm(x, r, w, p=0.4, **key)
+        return h * y
+
+    want = torch.autograd.grad(block(x, r).sum(), [x, r, w])
+    got = torch.autograd.grad(checkpoint(block, x, r, use_reentrant=False).sum(), [x, r, w])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_explicit_stream_needs_its_own_workspace():
     h, dy = torch.randn(8, 16, device="cuda"), torch.randn(8, 16, device="cuda")
     rstd, dw = torch.ones(8, device="cuda"), torch.empty(16, device="cuda")
