@@ -91,31 +91,37 @@ void fwd_type(Spread sp, int mode, bool same, const FwdArgs& a, hipStream_t s) {
     case 128: return fwd_mode<T, 128, 2>(mode, same, a, s);
     case 256: return fwd_mode<T, 256, 2>(mode, same, a, s);
     case 512: return fwd_mode<T, 512, 2>(mode, same, a, s);
-    default: return fwd_mode<T, 1024, 2>(mode, same, a, s);
+    // two workgroups of 1024 fit a compute unit up to 64 registers: with dropout not
+    // next to weights loaded up front (1024 x 16384 bf16, 29.2 us against 34.6)
+    default: return fwd_mode<T, 1024, 2>(mode, same && mode != DROPPED, a, s);
   }
 }
 
-template <typename T, int LANES, int NV>
+template <typename T, int LANES, int NV, int MODE>
+void launch_bwd(const BwdArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_norm_bwd<T, LANES, NV, kBwdThreads, MODE>), (unsigned)a.splits, kBwdThreads, 0, s, a);
+}
+
+template <typename T, int LANES>
 void bwd_mode(int mode, const BwdArgs& a, hipStream_t s) {
-  const unsigned groups = (unsigned)a.splits;
-  if (mode == PLAIN) hipLaunchKernelGGL((k_norm_bwd<T, LANES, NV, kBwdThreads, PLAIN>), groups, kBwdThreads, 0, s, a);
-  else if (mode == RESIDUAL) hipLaunchKernelGGL((k_norm_bwd<T, LANES, NV, kBwdThreads, RESIDUAL>), groups, kBwdThreads, 0, s, a);
-  else hipLaunchKernelGGL((k_norm_bwd<T, LANES, NV, kBwdThreads, DROPPED>), groups, kBwdThreads, 0, s, a);
+  if (mode == PLAIN) launch_bwd<T, LANES, 1, PLAIN>(a, s);
+  else if (mode == RESIDUAL) launch_bwd<T, LANES, 1, RESIDUAL>(a, s);
+  else launch_bwd<T, LANES, 1, DROPPED>(a, s);
 }
 
 template <typename T>
 void bwd_type(Spread sp, int mode, const BwdArgs& a, hipStream_t s) {
   if constexpr (!is_f32<T>)
-    if (sp.chunks == 2) return bwd_mode<T, 1024, 2>(mode, a, s);
+    if (sp.chunks == 2) return mode == PLAIN ? launch_bwd<T, 1024, 2, PLAIN>(a, s) : launch_bwd<T, 1024, 2, RESIDUAL>(a, s);
   switch (sp.lanes) {
-    case 8: return bwd_mode<T, 8, 1>(mode, a, s);
-    case 16: return bwd_mode<T, 16, 1>(mode, a, s);
-    case 32: return bwd_mode<T, 32, 1>(mode, a, s);
-    case 64: return bwd_mode<T, 64, 1>(mode, a, s);
-    case 128: return bwd_mode<T, 128, 1>(mode, a, s);
-    case 256: return bwd_mode<T, 256, 1>(mode, a, s);
-    case 512: return bwd_mode<T, 512, 1>(mode, a, s);
-    default: return bwd_mode<T, 1024, 1>(mode, a, s);
+    case 8: return bwd_mode<T, 8>(mode, a, s);
+    case 16: return bwd_mode<T, 16>(mode, a, s);
+    case 32: return bwd_mode<T, 32>(mode, a, s);
+    case 64: return bwd_mode<T, 64>(mode, a, s);
+    case 128: return bwd_mode<T, 128>(mode, a, s);
+    case 256: return bwd_mode<T, 256>(mode, a, s);
+    case 512: return bwd_mode<T, 512>(mode, a, s);
+    default: return bwd_mode<T, 1024>(mode, a, s);
   }
 }
 
@@ -213,7 +219,8 @@ int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
   const int64_t rows = in->rows, cols = in->cols;
   const size_t es = elem_size(in->dtype), ws = elem_size(in->wdtype);
   const bool any = rows > 0, params = in->dweight || in->dbias, grads = in->d || in->dx;
-  const int64_t splits = bwd_splits(rows, cols, in->dtype);
+  const bool dropping = in->dx != nullptr;
+  const int64_t splits = bwd_splits(rows, cols, in->dtype, dropping);
   Arrays ar;
   FO_TRY(ar.add(in->dy, "dy", false, any, rows, cols, in->dy_ld, es));
   FO_TRY(ar.add(in->dh, "dh", false, false, rows, cols, in->dh_ld, es));
@@ -239,9 +246,9 @@ int fo_norm_backward(const fo_norm_bwd* in, void* stream) {
   a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms; a.splits = (int)splits;
   a.inv_cols = (float)(1.0 / (double)cols);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const Spread sp = bwd_spread(cols, in->dtype);
+  const Spread sp = bwd_spread(cols, in->dtype, dropping);
   if (any && sp.lanes) {
-    const int mode = in->dx ? DROPPED : in->dh ? RESIDUAL : PLAIN;
+    const int mode = dropping ? DROPPED : in->dh ? RESIDUAL : PLAIN;
     if (!grads && !params) return FO_OK;
     if (in->dtype == FO_BF16) bwd_type<Bf16>(sp, mode, a, s);
     else if (in->dtype == FO_FP16) bwd_type<Fp16>(sp, mode, a, s);

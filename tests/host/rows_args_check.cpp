@@ -69,11 +69,13 @@ int main() {
     const int64_t n = (cols + 7) / 8;
     const Spread f = fwd_spread(cols);
     CHECK(f.lanes == 0 ? n > 2048 : (int64_t)f.lanes * f.chunks >= n && fwd_threads(f.lanes) % f.lanes == 0);
-    for (int dt : {(int)FO_BF16, (int)FO_FP16, (int)FO_F32}) {
-      const Spread b = bwd_spread(cols, dt);
-      CHECK(b.lanes == 0 ? n > (dt == FO_F32 ? 1024 : 2048) : (int64_t)b.lanes * b.chunks >= n && kBwdThreads % b.lanes == 0);
+    for (int call = 0; call < 6; ++call) {
+      const int dt = call % 3;
+      const bool dropping = call >= 3;
+      const Spread b = bwd_spread(cols, dt, dropping);
+      CHECK(b.lanes == 0 ? n > (dt == FO_F32 || dropping ? 1024 : 2048) : (int64_t)b.lanes * b.chunks >= n && kBwdThreads % b.lanes == 0);
       for (int64_t rows : {int64_t(0), int64_t(1), int64_t(7), int64_t(1000), int64_t(1) << 24, kMaxRows}) {
-        const int64_t s = bwd_splits(rows, cols, dt);
+        const int64_t s = bwd_splits(rows, cols, dt, dropping);
         CHECK(rows == 0 ? s == 0 : s >= 1 && s <= kColGroups);
         CHECK(2 * s * cols * 4 <= bwd_workspace(rows, cols));
         if (b.lanes) CHECK(s <= kBwdGroups && (s == kBwdGroups || s * (kBwdThreads / b.lanes) >= rows));
