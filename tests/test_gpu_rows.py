@@ -648,6 +648,41 @@ def test_training_steps_with_the_optimizer(release):
         assert all(not torch.equal(q, o) for q, o in zip(flat, before) if q.dim() == 2)
 
 
+def test_modules_under_the_optimizer():
+    """The modules as layers of a model FlashAdamW owns: their weights become theta',
+    every gradient has its type, and the weights move against the gradient."""
+    from precision_optimizer_state_amd import FlashAdamW
+    torch.manual_seed(2)
+    counter = nn.DropoutCounter(seed=5)
+    model = torch.nn.Sequential(torch.nn.Linear(48, 80, device="cuda"), nn.FlashLayerNorm(80, device="cuda"),
+                                nn.FlashDropout(0.1, counter), torch.nn.Linear(80, 24, device="cuda"),
+                                nn.FlashRMSNorm(24, device="cuda"))
+    opt = FlashAdamW(model.parameters(), lr=1e-2, weight_decay=0.0)
+    x, target = torch.randn(64, 48, device="cuda").bfloat16(), torch.randn(64, 24, device="cuda")
+    before = [opt.master_weights(q) for q in model.parameters()]
+    (model(x).float() - target).square().mean().backward()
+    grads = [q.grad.float() for q in model.parameters()]
+    assert counter.offset == 1
+    opt.step()
+    for q, old, g in zip(model.parameters(), before, grads):
+        assert q.dtype == q.grad.dtype == torch.bfloat16
+        # the first step of AdamW moves every weight by lr against its gradient's sign
+        step = opt.master_weights(q) - old
+        sure = g.abs() > 1e-6
+        assert sure.any() and (torch.sign(step[sure]) == -torch.sign(g[sure])).all()
+
+
+def test_device_state_is_added_to_the_key():
+    x = torch.ones(40, 100, device="cuda")
+    state = torch.tensor([3, -1], dtype=torch.int64, device="cuda")          # -1: the offset wraps
+    y = torch.empty_like(x)
+    B.fo_dropout(x, y, B.dropout_key(0.5, 7, 10, state))
+    assert np.array_equal((y != 0).cpu().numpy(), R.keep(40, 100, 0.5, 10, 9))
+    assert torch.equal(nn.dropout(x, 0.5, 7, 10, state), y)
+    h, _ = nn.dropout_add_rms_norm(x, torch.zeros_like(x), p=0.5, seed=7, offset=10, state=state)
+    assert torch.equal(h, y)
+
+
 # ---------------------------------------------------------------------------
 # refusals that need a device tensor
 # ---------------------------------------------------------------------------
