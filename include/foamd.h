@@ -116,7 +116,8 @@ extern "C" {
                                  NaN-only short last blocks keep a NaN scale, SGD momentum 0 as torch;
                               4: fo_hbm_probe takes a chunk size (and an in-place mode);
                               5: FO_COMPANDED4, 4-bit state codes;
-                              6: FO_COMPANDED_BF16SCALE, bfloat16 block scales */
+                              6: FO_COMPANDED_BF16SCALE, bfloat16 block scales; the row operators joined it
+                                 without a change to what was there */
 
 enum fo_status {
   FO_OK = 0,

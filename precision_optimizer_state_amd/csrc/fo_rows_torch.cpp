@@ -259,7 +259,8 @@ struct Norm : torch::autograd::Function<Norm> {
                                const Key& key, const MaybeTensor& state) {
     Forward f = norm_forward(x, value(residual), value(weight), value(bias), eps, static_cast<int>(kind), key,
                              value(state), true);
-    ctx->save_for_backward({f.h.defined() ? f.h : x, value(weight), f.stats, value(state)});
+    // a state that no mask came from may change before the backward pass
+    ctx->save_for_backward({f.h.defined() ? f.h : x, value(weight), f.stats, key.p != 0.0 ? value(state) : Tensor()});
     Saved::put(ctx, key, static_cast<int32_t>(kind), bias ? bias->scalar_type() : at::ScalarType::Undefined);
     ctx->set_materialize_grads(false);
     if (f.h.defined()) return {f.h, f.y};
