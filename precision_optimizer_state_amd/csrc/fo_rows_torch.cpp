@@ -5,10 +5,13 @@
 // a small call costs more on the host than on the GPU: a forward and backward
 // pass through a Python autograd.Function took 140-230 us of host time, whatever
 // the size.
+#include <ATen/CPUGeneratorImpl.h>
+#include <ATen/SavedTensorHooks.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/extension.h>
 
 #include <cstdint>
@@ -371,6 +374,28 @@ variable_list norm(const Tensor& x, const MaybeTensor& residual_arg, const Maybe
   return {f.y};
 }
 
+// ---------------------------------------------------------------------------
+// recomputed forward passes
+// ---------------------------------------------------------------------------
+// Whether a backward pass may run the present forward code again, or is doing so:
+// activation checkpointing runs a function first without gradients or under hooks
+// on saved tensors, and again inside the backward pass, from the same state of
+// torch's CPU generator.  For such a call, a number drawn from that generator
+// (the same one both times) and whether this is inside a backward pass; None for
+// any other.
+std::optional<std::pair<int64_t, bool>> recomputation() {
+  const bool backward = torch::autograd::get_current_graph_task_id() != -1;
+  if (!backward) {
+    if (c10::InferenceMode::is_enabled()) return std::nullopt;
+    if (at::GradMode::is_enabled() && !at::SavedTensorDefaultHooks::get_hooks(/*ignore_is_tracing=*/true))
+      return std::nullopt;
+  }
+  at::Generator gen = at::detail::getDefaultCPUGenerator();
+  const std::lock_guard<std::mutex> lock(gen.mutex());
+  const uint64_t drawn = at::check_generator<at::CPUGeneratorImpl>(gen)->random64();
+  return std::pair<int64_t, bool>(static_cast<int64_t>(drawn >> 1), backward);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
@@ -378,6 +403,7 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   m.def("dropout", &dropout, py::arg("x"), py::arg("p"), py::arg("seed"), py::arg("offset"), py::arg("state"));
   m.def("norm", &norm, py::arg("x"), py::arg("residual"), py::arg("weight"), py::arg("bias"), py::arg("eps"),
         py::arg("kind"), py::arg("p"), py::arg("seed"), py::arg("offset"), py::arg("state"));
+  m.def("recomputation", &recomputation);
   // FoError, raised with (code, message)
   static py::object error;
   m.def("set_error", [](py::object cls) { error = std::move(cls); });

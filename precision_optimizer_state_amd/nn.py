@@ -73,20 +73,46 @@ class DropoutCounter:
     must be called between replays (or at the end of the captured step), never
     between a forward pass and its backward pass.
 
-    Code that runs a forward function again for its backward pass (activation
-    checkpointing) must take the arguments from next() outside that function
-    and pass them in, so that both runs find the same mask."""
+    A forward pass that a backward pass runs again (activation checkpointing)
+    finds the same arguments: next() ties those it gives out without gradients
+    or under hooks on saved tensors, where a first run cannot be told from any
+    other call, to one number drawn from torch's CPU generator, whose state
+    torch.utils.checkpoint restores for the second run.  The same state of that
+    generator then gives the same arguments again, whoever set it.  Inside a
+    backward pass next() refuses a state that it has given nothing for
+    (preserve_rng_state=False; a new forward pass in a hook): such code takes
+    the arguments before and passes them in."""
 
     _STRIDE = 1 << 32       # offsets of one replay to those of the next
+    _REMEMBERED = 1 << 16   # calls between a first run and its recomputation, at most
 
     def __init__(self, seed: int, offset: int = 0, device=None):
         self.seed, self.offset = int(seed), int(offset)
         self.state = None if device is None else torch.zeros(2, dtype=torch.int64, device=device)
 
     def next(self) -> dict:
-        args = {"seed": self.seed, "offset": self.offset, "state": self.state}
+        again = (_ext or _load()).recomputation()
+        if again is None:
+            seed, offset = self._fresh()
+        else:
+            drawn, backward = again
+            given = self.__dict__.setdefault("_given", {})
+            if drawn not in given:
+                if backward:
+                    raise RuntimeError(
+                        "a dropout call inside a backward pass recomputes no forward call that this counter knows, so its "
+                        "mask cannot be found again: keep torch's generator state (preserve_rng_state=True), or take "
+                        "the arguments from next() outside the recomputed function")
+                given[drawn] = self._fresh()
+                if len(given) > self._REMEMBERED:
+                    del given[next(iter(given))]
+            seed, offset = given[drawn]
+        return {"seed": seed, "offset": offset, "state": self.state}
+
+    def _fresh(self):
+        offset = self.offset
         self.offset += 1
-        return args
+        return self.seed, offset
 
     def advance(self) -> None:
         if self.state is None:
@@ -179,7 +205,9 @@ class FlashRMSNorm(torch.nn.RMSNorm):
 
 class FlashDropout(torch.nn.Module):
     """torch.nn.Dropout on dropout(); `counter` (shared between modules or not)
-    gives every call its mask."""
+    gives every call its mask, and a recomputed call
+    the mask of its first run.  What resumes the masks is the counter's
+    state_dict(), saved beside the model's, which holds nothing of it."""
 
     def __init__(self, p: float, counter: DropoutCounter):
         super().__init__()

@@ -1,0 +1,134 @@
+"""DropoutCounter without a GPU: keys in recomputed functions (activation
+checkpointing).  Masks come from the oracle, so any wrong key is a wrong
+gradient here."""
+
+import pytest
+import torch
+from torch.utils.checkpoint import checkpoint
+
+from oracle import rows as R
+from precision_optimizer_state_amd import nn
+
+
+def drop(x, key, p=0.5):
+    """What nn.dropout computes, in torch operations on the CPU."""
+    keep = torch.from_numpy(R.keep(*x.shape, p, key["seed"], key["offset"]))
+    return torch.where(keep, x * R.scale(p), torch.zeros_like(x))
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+@pytest.mark.parametrize("noise", [False, True])
+def test_recomputed_segments_find_their_masks(reentrant, noise):
+    """Three segments of two dropouts each; with `noise` they draw from torch's generator too.
+    The masks are linear, so the gradient of x is the product of the masks and scales."""
+    counter, made = nn.DropoutCounter(seed=7), []
+
+    def segment(x):
+        if noise:
+            x = x + 0 * torch.rand(3)[0]
+        for _ in range(2):
+            key = counter.next()
+            made.append(key["offset"])
+            x = drop(x, key)
+        return x
+
+    x = torch.randn(40, 9, requires_grad=True)
+    y = x
+    for _ in range(3):
+        y = checkpoint(segment, y, use_reentrant=reentrant)
+    assert made == list(range(6)) and counter.offset == 6
+    g, = torch.autograd.grad(y.sum(), x) if not reentrant else (y.sum().backward(), x.grad)[1:]
+    assert sorted(made[6:]) == list(range(6)) and counter.offset == 6
+    want = torch.ones_like(x)
+    for k in range(6):
+        want = drop(want, {"seed": 7, "offset": k})
+    assert torch.equal(g, want)
+    assert counter.next()["offset"] == 6
+
+
+@pytest.mark.parametrize("outer", [True, False])
+@pytest.mark.parametrize("inner", [True, False])
+def test_nested_checkpoints(outer, inner):
+    counter = nn.DropoutCounter(seed=1)
+
+    def part(x):
+        return drop(x, counter.next())
+
+    def whole(x):
+        return part(checkpoint(part, part(x), use_reentrant=inner))
+
+    x = torch.randn(30, 5, requires_grad=True)
+    checkpoint(whole, x, use_reentrant=outer).sum().backward()
+    want = torch.ones_like(x)
+    for k in range(3):
+        want = drop(want, {"seed": 1, "offset": k})
+    assert torch.equal(x.grad, want) and counter.offset == 3
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_two_forward_passes_before_their_backward_passes(reentrant):
+    counter = nn.DropoutCounter(seed=2)
+    xs = [torch.randn(30, 5, requires_grad=True) for _ in range(2)]
+    ys = [checkpoint(lambda t: drop(t, counter.next()), x, use_reentrant=reentrant) for x in xs]
+    for i in (1, 0):
+        ys[i].sum().backward()
+        assert torch.equal(xs[i].grad, drop(torch.ones(30, 5), {"seed": 2, "offset": i}))
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_a_recomputation_without_the_generator_state_is_refused(reentrant):
+    counter = nn.DropoutCounter(seed=3)
+    x = torch.randn(30, 5, requires_grad=True)
+    y = checkpoint(lambda t: drop(t, counter.next()), x, use_reentrant=reentrant, preserve_rng_state=False)
+    with pytest.raises(RuntimeError, match="recomput"):
+        y.sum().backward()
+    # with a key from outside it works
+    key = counter.next()
+    y = checkpoint(lambda t: drop(t, key), x, use_reentrant=reentrant, preserve_rng_state=False)
+    x.grad = None
+    y.sum().backward()
+    assert torch.equal(x.grad, drop(torch.ones(30, 5), key))
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_the_same_generator_state_gives_the_same_key(reentrant):
+    # a program that seeds torch before every forward pass: both recomputations find their masks
+    counter, xs, ys = nn.DropoutCounter(seed=4), [], []
+    for _ in range(2):
+        torch.manual_seed(0)
+        xs.append(torch.randn(30, 5, requires_grad=True))
+        ys.append(checkpoint(lambda t: drop(t, counter.next()), xs[-1], use_reentrant=reentrant))
+    for x, y in zip(xs, ys):
+        with torch.no_grad():
+            kept = y != 0
+        y.sum().backward()
+        assert torch.equal(x.grad != 0, kept)
+
+
+def test_ordinary_calls_leave_the_generator_alone():
+    counter = nn.DropoutCounter(seed=5, offset=3)
+    before = torch.get_rng_state()
+    assert [counter.next()["offset"] for _ in range(3)] == [3, 4, 5]
+    assert torch.equal(torch.get_rng_state(), before)
+    with torch.no_grad():
+        assert [counter.next()["offset"] for _ in range(3)] == [6, 7, 8]
+    with torch.inference_mode():
+        assert counter.next()["offset"] == 9
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t):
+        assert [counter.next()["offset"] for _ in range(2)] == [10, 11]
+    assert counter.state_dict() == {"seed": 5, "offset": 12, "state": None}
+
+
+def test_remembered_keys_are_bounded():
+    counter = nn.DropoutCounter(seed=6)
+    with torch.no_grad():
+        for _ in range(nn.DropoutCounter._REMEMBERED + 10):
+            counter.next()
+    assert len(counter._given) == nn.DropoutCounter._REMEMBERED
+    # a forward pass longer than that is refused in its backward pass, not given other masks
+    x = torch.randn(2, 2, requires_grad=True)
+    counter._given.clear()
+    y = checkpoint(lambda t: t * counter.next()["offset"], x, use_reentrant=True)
+    counter._given.clear()
+    with pytest.raises(RuntimeError, match="recomput"):
+        y.sum().backward()
