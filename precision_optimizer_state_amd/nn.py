@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -36,6 +37,7 @@ from . import binding as B
 EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "fo_rows_torch.so")
 _ext = None
 _M64 = (1 << 64) - 1
+_lock = threading.Lock()        # of all counters (one of its own would keep a counter from being copied)
 
 
 def _load():
@@ -66,7 +68,7 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, state: torch.
 
 class DropoutCounter:
     """Seeds and offsets for dropout calls: next() gives the arguments of one
-    call, a fresh offset each time.
+    call, a fresh offset each time, also to calls from several threads.
 
     With `device`, it also holds a state tensor there: a captured graph keeps
     the offsets it was captured with and draws new masks after advance(), which
@@ -92,21 +94,22 @@ class DropoutCounter:
 
     def next(self) -> dict:
         again = (_ext or _load()).recomputation()
-        if again is None:
-            seed, offset = self._fresh()
-        else:
-            drawn, backward = again
-            given = self.__dict__.setdefault("_given", {})
-            if drawn not in given:
-                if backward:
-                    raise RuntimeError(
-                        "a dropout call inside a backward pass recomputes no forward call that this counter knows, so its "
-                        "mask cannot be found again: keep torch's generator state (preserve_rng_state=True), or take "
-                        "the arguments from next() outside the recomputed function")
-                given[drawn] = self._fresh()
-                if len(given) > self._REMEMBERED:
-                    del given[next(iter(given))]
-            seed, offset = given[drawn]
+        with _lock:
+            if again is None:
+                seed, offset = self._fresh()
+            else:
+                drawn, backward = again
+                given = self.__dict__.setdefault("_given", {})
+                if drawn not in given:
+                    if backward:
+                        raise RuntimeError(
+                            "a dropout call inside a backward pass recomputes no forward call that this counter knows, so "
+                            "its mask cannot be found again: keep torch's generator state (preserve_rng_state=True), or "
+                            "take the arguments from next() outside the recomputed function")
+                    given[drawn] = self._fresh()
+                    if len(given) > self._REMEMBERED:
+                        del given[next(iter(given))]
+                seed, offset = given[drawn]
         return {"seed": seed, "offset": offset, "state": self.state}
 
     def _fresh(self):

@@ -1,6 +1,9 @@
 """DropoutCounter without a GPU: keys in recomputed functions (activation
-checkpointing).  Masks come from the oracle, so any wrong key is a wrong
+checkpointing) and between threads.  Masks come from the oracle, so any wrong key is a wrong
 gradient here."""
+
+import threading
+import time
 
 import pytest
 import torch
@@ -132,3 +135,21 @@ def test_remembered_keys_are_bounded():
     counter._given.clear()
     with pytest.raises(RuntimeError, match="recomput"):
         y.sum().backward()
+
+
+def test_threads_get_keys_of_their_own():
+    class Slow(int):
+        """Lets other threads run between the reading and the writing of the offset."""
+        def __add__(self, other):
+            time.sleep(0.002)
+            return Slow(int(self) + other)
+
+    counter, got = nn.DropoutCounter(seed=8), []
+    counter.offset = Slow(0)
+    threads = [threading.Thread(target=lambda: got.extend(counter.next()["offset"] for _ in range(5)))
+               for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(got) == list(range(20))
