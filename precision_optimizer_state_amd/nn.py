@@ -26,6 +26,7 @@ a constant distance are copied first.  Gradients of gradients are not provided.
 
 from __future__ import annotations
 
+import copy
 import importlib.util
 import os
 import threading
@@ -209,7 +210,8 @@ class FlashRMSNorm(torch.nn.RMSNorm):
 class FlashDropout(torch.nn.Module):
     """torch.nn.Dropout on dropout(); `counter` (shared between modules or not)
     gives every call its mask, and a recomputed call
-    the mask of its first run.  What resumes the masks is the counter's
+    the mask of its first run.  Copies of the module share the counter, so they
+    draw masks of their own.  What resumes the masks is the counter's
     state_dict(), saved beside the model's, which holds nothing of it."""
 
     def __init__(self, p: float, counter: DropoutCounter):
@@ -222,6 +224,12 @@ class FlashDropout(torch.nn.Module):
         if not self.training or self.p == 0.0:
             return x
         return dropout(x, self.p, **self.counter.next())
+
+    def __deepcopy__(self, memo):
+        memo.setdefault(id(self.counter), self.counter)
+        new = memo[id(self)] = self.__class__.__new__(self.__class__)
+        new.__dict__.update(copy.deepcopy(self.__dict__, memo))
+        return new
 
     def extra_repr(self) -> str:
         return f"p={self.p}"

@@ -1,6 +1,8 @@
 """FlashDropout and the counter's keys in recomputed forward passes on the GPU,
 against the same model without recomputation."""
 
+import copy
+
 import pytest
 import torch
 from torch.utils.checkpoint import checkpoint
@@ -53,3 +55,11 @@ def test_joins_with_keys_taken_inside(reentrant):
         (h * y).sum().backward()
         out.append((h, y, x.grad, w.grad))
     assert counter.offset == 3 and all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_copies_of_a_module_draw_masks_of_their_own():
+    block = torch.nn.Sequential(nn.FlashDropout(0.5, nn.DropoutCounter(seed=2)))
+    x = torch.ones(64, 64, device="cuda")
+    masks = [copy.deepcopy(block)(x) for _ in range(3)] + [block(x)]
+    for i, a in enumerate(masks):
+        assert torch.equal(a, nn.dropout(x, 0.5, 2, i))

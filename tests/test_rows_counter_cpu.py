@@ -1,7 +1,8 @@
-"""DropoutCounter without a GPU: keys in recomputed functions (activation
-checkpointing) and between threads.  Masks come from the oracle, so any wrong key is a wrong
-gradient here."""
+"""DropoutCounter and FlashDropout without a GPU: keys in recomputed functions
+(activation checkpointing), between threads and in copies of a module.  Masks
+come from the oracle, so any wrong key is a wrong gradient here."""
 
+import copy
 import threading
 import time
 
@@ -153,3 +154,19 @@ def test_threads_get_keys_of_their_own():
     for t in threads:
         t.join()
     assert sorted(got) == list(range(20))
+
+
+def test_copied_modules_share_the_counter_and_not_the_masks():
+    counter = nn.DropoutCounter(seed=9)
+    block = torch.nn.Sequential(torch.nn.Linear(4, 4), nn.FlashDropout(0.25, counter))
+    layers = torch.nn.ModuleList(copy.deepcopy(block) for _ in range(3))
+    keys = [layer[1].counter.next()["offset"] for layer in layers] + [block[1].counter.next()["offset"]]
+    assert keys == [0, 1, 2, 3]
+    assert layers[0][0].weight is not block[0].weight and layers[0][1] is not block[1]
+    assert layers[0][1].p == 0.25 and copy.copy(block[1]).counter is counter
+    layers[0][1].eval()
+    assert block[1].training
+    # a counter that is copied by itself is another one
+    other = copy.deepcopy(counter)
+    other.next()
+    assert counter.offset == 4 and other.offset == 5
