@@ -66,6 +66,14 @@ void check_device(const Tensor& t) {
                     static_cast<int>(dev));
 }
 
+// Kernels are launched on addresses, so a tangent that rides on an input would be
+// left out of what comes back: no derivative instead of an error.
+void check_plain(std::initializer_list<const Tensor*> inputs) {
+  for (const Tensor* t : inputs)
+    TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(/*level=*/0).defined(),
+                                "the row operators have no forward-mode derivatives");
+}
+
 void* current_stream() { return c10::hip::getCurrentHIPStream().stream(); }
 
 // Under capture, the gradient of an input whose place in the autograd graph was
@@ -199,6 +207,7 @@ struct Dropout : torch::autograd::Function<Dropout> {
     return drop(x, key, value(state));
   }
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    check_plain({&grads[0]});
     return once({drop(grads[0], Saved::get(ctx)->key, ctx->get_saved_variables()[0]), Tensor(), Tensor()});
   }
 };
@@ -207,6 +216,7 @@ Tensor dropout(const Tensor& x, double p, uint64_t seed, uint64_t offset, const 
   const Key key{p, seed, offset};
   check_key(key, value(state));
   if (p == 0.0) return x;
+  check_plain({&x});
   check_device(x);
   dtype_of(x);
   if (at::GradMode::is_enabled() && x.requires_grad()) {
@@ -277,6 +287,7 @@ struct Norm : torch::autograd::Function<Norm> {
     const Key& key = args->key;
     const bool join = grads.size() == 2;
     const Tensor dy = grads.back(), dh = join ? grads[0] : Tensor();
+    check_plain({&dy, &dh});
     // the inputs that were there, in the order of forward's arguments
     size_t input = 0;
     const bool need_x = ctx->needs_input_grad(input++);
@@ -343,6 +354,7 @@ variable_list norm(const Tensor& x, const MaybeTensor& residual_arg, const Maybe
   const Tensor residual = value(residual_arg), weight = value(weight_arg), bias = value(bias_arg);
   const Tensor state = value(state_arg);
   check_key(key, state);
+  check_plain({&x, &residual, &weight, &bias});
   TORCH_CHECK_VALUE(x.dim() > 0 && x.size(-1) > 0,
                     "a norm needs a last dimension of at least one element, got shape ", sizes(x));
   check_device(x);

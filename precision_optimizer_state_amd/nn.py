@@ -21,7 +21,8 @@ torch and never synchronise, so they can be captured into HIP graphs (a captured
 call refuses leaves that an eager autograd graph, still alive, has used on the
 default stream: capture with detached leaves).  Norms are over the last
 dimension.  Inputs whose rows are not consecutive elements at
-a constant distance are copied first.  Gradients of gradients are not provided.
+a constant distance are copied first.  Gradients of gradients and forward-mode
+derivatives are not provided (such calls are refused).
 """
 
 from __future__ import annotations
