@@ -7,6 +7,8 @@
 // the size.
 #include <ATen/CPUGeneratorImpl.h>
 #include <ATen/SavedTensorHooks.h>
+#include <ATen/TracerMode.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
@@ -66,9 +68,18 @@ void check_device(const Tensor& t) {
                     static_cast<int>(dev));
 }
 
-// Kernels are launched on addresses, so a tangent that rides on an input would be
-// left out of what comes back: no derivative instead of an error.
+// A tracer (make_fx, torch.jit.trace) sees the outputs' allocations and no launch.
+bool traced() {
+  using Modes = c10::impl::TorchDispatchModeTLS;
+  return at::tracer::impl::is_dispatch_enabled() || c10::impl::tls_is_dispatch_key_included(c10::DispatchKey::PreDispatch) ||
+         (Modes::any_modes_set() && Modes::get_mode(c10::impl::TorchDispatchModeKey::PROXY));
+}
+
+// Kernels are launched on addresses: a tangent that rides on an input would be
+// left out of what comes back, no derivative instead of an error, and a trace
+// would replay as memory that nothing has written.
 void check_plain(std::initializer_list<const Tensor*> inputs) {
+  TORCH_CHECK_NOT_IMPLEMENTED(!traced(), "the row operators cannot be traced (make_fx, torch.jit.trace)");
   for (const Tensor* t : inputs)
     TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(/*level=*/0).defined(),
                                 "the row operators have no forward-mode derivatives");

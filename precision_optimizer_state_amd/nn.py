@@ -22,7 +22,8 @@ call refuses leaves that an eager autograd graph, still alive, has used on the
 default stream: capture with detached leaves).  Norms are over the last
 dimension.  Inputs whose rows are not consecutive elements at
 a constant distance are copied first.  Gradients of gradients and forward-mode
-derivatives are not provided (such calls are refused).
+derivatives are not provided, and the functions cannot be traced by make_fx or
+torch.jit.trace: such calls are refused.
 """
 
 from __future__ import annotations

@@ -1,5 +1,5 @@
-"""Forward-mode derivatives meet the row operators on the GPU: a tangent is
-refused, never dropped."""
+"""Forward-mode derivatives and tracers meet the row operators on the GPU: a
+tangent or a trace is refused; neither comes back without the operator's part."""
 
 import pytest
 import torch
@@ -45,3 +45,29 @@ def test_forward_mode_through_a_backward_pass_is_refused(op):
         dy = fwAD.make_dual(torch.ones_like(y), torch.ones_like(y))
         with pytest.raises(NotImplementedError, match="forward-mode"):
             torch.autograd.grad(y, args[0], dy)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("pre_dispatch", [False, True])
+def test_tracers_are_refused(op, pre_dispatch):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    args = arguments()
+    want = calls(*args)[op]()
+    with pytest.raises(NotImplementedError, match="traced"):
+        make_fx(lambda t: calls(t, *args[1:])[op](), pre_dispatch=pre_dispatch)(args[0])
+    with pytest.raises(NotImplementedError, match="traced"):
+        torch.jit.trace(lambda t: calls(t, *args[1:])[op](), args[0], check_trace=False)
+    with pytest.raises(Exception):                                # fake tensors have no memory
+        make_fx(lambda t: calls(t, *args[1:])[op](), tracing_mode="fake")(args[0])
+    assert torch.equal(calls(*args)[op](), want)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_a_traced_backward_pass_is_refused(op):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    args = arguments()
+    args[0].requires_grad_(True)
+    y = calls(*args)[op]()
+    with pytest.raises(NotImplementedError, match="traced"):
+        make_fx(lambda dy: torch.autograd.grad(y, args[0], dy, retain_graph=True)[0])(torch.ones_like(y))
+    torch.autograd.grad(y, args[0], torch.ones_like(y))

@@ -1,5 +1,6 @@
-"""Forward-mode derivatives of the row operators are refused before anything else
-is looked at, so host tensors do here."""
+"""Calls of the row operators that torch would have to see through, and cannot:
+forward-mode derivatives and tracers.  They are refused before anything else is
+looked at, so host tensors do here."""
 
 import pytest
 import torch
@@ -26,3 +27,38 @@ def test_forward_mode_is_refused(op, which, grad):
             calls(*args)[op]()
         x = args[0]
         assert nn.dropout(x, 0.0, 1) is x
+
+
+OPS = ["dropout", "layer_norm", "rms_norm", "join_layer", "join_rms"]
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("pre_dispatch", [False, True])
+def test_make_fx_is_refused(op, grad, pre_dispatch):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    r, w, b = torch.randn(4, 8), torch.ones(8), torch.zeros(8)
+    x = torch.randn(4, 8).requires_grad_(grad)
+    with pytest.raises(NotImplementedError, match="traced"):
+        make_fx(lambda t: calls(t, r, w, b)[op](), pre_dispatch=pre_dispatch)(x)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_jit_trace_is_refused(op):
+    r, w, b = torch.randn(4, 8), torch.ones(8), torch.zeros(8)
+    with pytest.raises(NotImplementedError, match="traced"):
+        torch.jit.trace(lambda t: calls(t, r, w, b)[op](), torch.randn(4, 8), check_trace=False)
+
+
+def test_other_modes_are_let_through():
+    # a dispatch mode that only watches reaches the check of the device
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            return func(*args, **(kwargs or {}))
+
+    with Watch(), pytest.raises(ValueError, match="GPU"):
+        nn.rms_norm(torch.randn(4, 8))
+    with pytest.raises(ValueError, match="GPU"):
+        nn.rms_norm(torch.randn(4, 8))
