@@ -323,6 +323,8 @@ def _rows_in(name, t, shape=None, dtype=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if t.is_neg():              # its memory holds the other sign
+        raise ValueError(f"{name} is a negated view: resolve_neg() it first")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"the elements of a row of {name} must be consecutive")
     return _addr(t), t.stride(0)
@@ -333,6 +335,8 @@ def _rows_out(name, t, shape, dtype):
         return None
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if t.is_neg():
+        raise ValueError(f"{name} is a negated view: resolve_neg() it first")
     return _ptr(t)
 
 
@@ -355,6 +359,8 @@ def dropout_key(p, seed, offset=0, state=None) -> DropoutKey:
         import torch
         if state.dtype != torch.int64 or state.numel() != 2:
             raise ValueError("the dropout state must hold 2 int64")
+        if state.is_neg():
+            raise ValueError("the dropout state is a negated view")
     key = DropoutKey(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1), _ptr(state).value)
     key._state = state
     return key

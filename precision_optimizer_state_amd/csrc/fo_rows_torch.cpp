@@ -103,6 +103,10 @@ void check_capture(std::initializer_list<const Tensor*> inputs) {
   }
 }
 
+// A view that torch negates when it reads it (the imaginary part of a conjugate)
+// holds the other sign in memory.
+Tensor resolved(const Tensor& t) { return t.is_neg() ? t.resolve_neg() : t; }
+
 // A tensor as a matrix: cols its last dimension, rows everything before.  The
 // tensor's own memory where its rows are consecutive elements at a constant
 // distance, else a packed copy (held here).
@@ -111,7 +115,8 @@ struct Rows {
   void* ptr;
   int64_t rows, cols, ld;
 
-  explicit Rows(const Tensor& t) : held(t) {
+  explicit Rows(const Tensor& any) : held(resolved(any)) {
+    const Tensor t = held;
     cols = t.dim() ? t.size(-1) : 1;
     rows = cols ? t.numel() / cols : 0;
     ld = cols;
@@ -140,7 +145,7 @@ struct Rows {
 
 void* address(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-Tensor packed(const Tensor& t) { return t.defined() ? t.contiguous() : t; }
+Tensor packed(const Tensor& t) { return t.defined() ? resolved(t).contiguous() : t; }
 
 Tensor empty_like_shape(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
@@ -178,6 +183,7 @@ void check_key(const Key& k, const Tensor& state) {
   if (!state.defined()) return;
   TORCH_CHECK_VALUE(state.scalar_type() == at::kLong && state.numel() == 2 && state.is_contiguous(),
                     "the dropout state must hold 2 int64");
+  TORCH_CHECK_VALUE(!state.is_neg(), "the dropout state is a negated view");
   check_device(state);
 }
 
