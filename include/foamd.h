@@ -435,8 +435,11 @@ typedef struct fo_norm_fwd {
  *   h = residual + dropout(x), rounded to dtype (h = x without a residual)
  *   m = mean(h) (RMS norm: 0);  r = 1 / sqrt(mean((h - m)^2) + eps)
  *   y = (h - m) * r * weight + bias
- * The statistics are taken of the rounded h, from its values less their mean;
- * rows whose squares overflow float32 (values past 1.8e19) get r = 0.
+ * The statistics are taken of the rounded h, from its values less their mean.
+ * Their float32 sums are scaled by a power of 4 near 1 / cols: a finite row's
+ * mean never overflows short of values of 1e38, and a row whose mean square
+ * does (values past 1.8e19) gets r = 0, so y = bias.  With eps = 0 r is as
+ * accurate as elsewhere for mean squares of at least 4 cols 2^-126.
  * rows == 0 is a no-op.  Errors: FO_EINVAL, FO_EALIAS, FO_EHIP.
  */
 int fo_norm_forward(const fo_norm_fwd* args, void* stream);

@@ -185,7 +185,10 @@ int fo_norm_forward(const fo_norm_fwd* in, void* stream) {
   a.h = in->h; a.y = in->y; a.mean = in->mean; a.rstd = in->rstd;
   a.rows = rows; a.x_ld = in->x_ld; a.residual_ld = in->residual_ld;
   a.cols = (int)cols; a.wdtype = in->wdtype; a.rms = rms;
-  a.eps = (float)in->eps; a.inv_cols = (float)(1.0 / (double)cols);
+  const int k = quarter_log(cols);
+  a.eps = (float)in->eps;
+  a.sum_scale = std::ldexp(1.0f, -2 * k); a.square_scale = std::ldexp(1.0f, -k);
+  a.mean_scale = std::ldexp((float)(1.0 / (double)cols), 2 * k);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int mode = !in->residual ? PLAIN : a.dropping ? DROPPED : RESIDUAL;
   const bool same = in->wdtype == in->dtype || (!in->weight && !in->bias);

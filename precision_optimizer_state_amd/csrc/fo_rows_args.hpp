@@ -26,6 +26,13 @@ inline int shape_ok(int64_t rows, int64_t cols) {
   return FO_OK;
 }
 
+// The smallest k with 4^k >= cols (see FwdArgs)
+inline int quarter_log(int64_t cols) {
+  int k = 0;
+  while ((int64_t(1) << 2 * k) < cols) ++k;
+  return k;
+}
+
 // The arrays of one call: checked one by one, then the outputs against all.
 struct Arrays {
   struct Span { uintptr_t lo, hi; bool out; const char* name; };

@@ -36,7 +36,12 @@ struct FwdArgs {
   float *mean, *rstd;
   int64_t rows, first_row, x_ld, residual_ld;     // first_row: of this launch (k_norm_fwd)
   int cols, wdtype, rms, dropping;
-  float eps, inv_cols;
+  float eps;
+  // Sums over a row are those of values times sum_scale = 4^-k and of squares of
+  // values times square_scale = 2^-k, with 4^k the first power of 4 that reaches cols:
+  // they overflow only where the mean itself would.  mean_scale = 4^k / cols makes
+  // means of them.  Powers of two commute with every rounding of normal numbers.
+  float sum_scale, square_scale, mean_scale;
   DropArgs drop;
 };
 
@@ -262,8 +267,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {                  // 0 past the row's end
       const float f = elem<T>(x[v], j);
-      if (a.rms) q = fmaf(f, f, q);
-      else s += f;
+      if (a.rms) { const float t = f * a.square_scale; q = fmaf(t, t, q); }
+      else s = fmaf(f, a.sum_scale, s);
     }
   }
   float mean = 0.0f;
@@ -274,12 +279,13 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
       __syncthreads();
       s = waves_sum<W>(red[0][grp]);
     }
-    mean = s * a.inv_cols;
+    mean = s * a.mean_scale;
+    const float shift = -mean * a.square_scale;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = j < cnt[v] ? elem<T>(x[v], j) - mean : 0.0f;
+        const float t = j < cnt[v] ? fmaf(elem<T>(x[v], j), a.square_scale, shift) : 0.0f;
         q = fmaf(t, t, q);
       }
   }
@@ -289,7 +295,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
     __syncthreads();
     q = waves_sum<W>(red[1][grp]);
   }
-  const float rstd = rsqrt_of(q * a.inv_cols + a.eps);
+  const float rstd = rsqrt_of(q * a.mean_scale + a.eps);
   if (live && lane == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
@@ -493,21 +499,25 @@ __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < cnt) s += a.rms ? elem<T>(c, j) * elem<T>(c, j) : elem<T>(c, j);
+        if (j < cnt) {
+          const float f = elem<T>(c, j), t = f * a.square_scale;
+          s += a.rms ? t * t : f * a.sum_scale;
+        }
     }
-    s = block_sum<BLOCK>(s, red) * a.inv_cols;
+    s = block_sum<BLOCK>(s, red) * a.mean_scale;
     float mean = 0.0f, var = s;
     if (!a.rms) {
       mean = s;
+      const float shift = -mean * a.square_scale;
       float q = 0.0f;
       for (int c0 = threadIdx.x * 8; c0 < a.cols; c0 += BLOCK * 8) {
         const int cnt = a.cols - c0;
         const Chunk<T> c = load_chunk<T>(src + c0, cnt);       // this thread's own stores, or x
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j < cnt) { const float t = elem<T>(c, j) - mean; q += t * t; }
+          if (j < cnt) { const float t = fmaf(elem<T>(c, j), a.square_scale, shift); q += t * t; }
       }
-      var = block_sum<BLOCK>(q, red) * a.inv_cols;
+      var = block_sum<BLOCK>(q, red) * a.mean_scale;
     }
     const float rstd = rsqrt_of(var + a.eps);
     if (threadIdx.x == 0) {
