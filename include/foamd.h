@@ -366,7 +366,8 @@ int fo_selftest(int what, uint32_t lo, uint64_t count, uint64_t* mismatches, voi
  * Data is a matrix of `rows` rows of `cols` elements of one type (`dtype`:
  * FO_BF16, FO_FP16 or FO_F32; elements of a row are consecutive).  Inputs have
  * a row stride in elements (`*_ld`, >= 0; 0 repeats one row); outputs are
- * packed (row stride = cols).  rows is at most 2^40, cols at most 2^26.
+ * packed (row stride = cols).  rows is at most 2^40, cols at most 2^26 (2^40 for
+ * fo_dropout).
  * Differing from the conventions above: rows may begin at any element, so
  * arrays need only their element's alignment (the workspace 16 bytes), and no
  * call allocates, synchronises or keeps anything: all may be captured into a

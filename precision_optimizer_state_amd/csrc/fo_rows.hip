@@ -135,19 +135,19 @@ int fo_dropout(const void* x, int64_t x_ld, void* y, int64_t rows, int64_t cols,
   if (!key) return fail(FO_EINVAL, "key is NULL");
   if (!dtype_ok(dtype)) return fail(FO_EINVAL, "bad element type %d", dtype);
   if (rows == 0 || cols == 0) return rows < 0 || cols < 0 ? fail(FO_EINVAL, "negative size") : FO_OK;
-  FO_TRY(shape_ok(rows, cols));
+  FO_TRY(drop_shape_ok(rows, cols));
   DropoutArgs a = {};
   FO_TRY(drop_args(key, &a.drop));
   Arrays ar;
   FO_TRY(ar.add(x, "x", false, true, rows, cols, x_ld, elem_size(dtype)));
   FO_TRY(ar.add(y, "y", true, true, rows, cols, cols, elem_size(dtype)));
   FO_TRY(ar.disjoint());
-  a.x = x; a.y = y; a.rows = rows; a.x_ld = x_ld; a.cols = (int)cols;
+  a.x = x; a.y = y; a.rows = rows; a.x_ld = x_ld; a.cols = cols;
   const int64_t chunks = rows * ((cols + 7) / 8);
   const unsigned groups = grid_of((chunks + BLOCK * DROP_PER - 1) / (BLOCK * DROP_PER));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (cols % 8 == 0 && (x_ld == cols || rows == 1)) drop_launch<true, int64_t>(dtype, groups, a, s);
-  else if (chunks < (int64_t(1) << 31)) drop_launch<false, uint32_t>(dtype, groups, a, s);
+  else if (chunks < (int64_t(1) << 31) && cols <= kMaxCols) drop_launch<false, uint32_t>(dtype, groups, a, s);
   else drop_launch<false, int64_t>(dtype, groups, a, s);
   return launch_check("dropout launch");
 }

@@ -14,15 +14,24 @@
 namespace fo {
 namespace rows {
 
-constexpr int64_t kMaxCols = int64_t(1) << 26;     // k_norm_bwd_reduce takes 32 threads per column
+constexpr int64_t kMaxCols = int64_t(1) << 26;     // of norms: k_norm_bwd_reduce takes 32 threads per column
+constexpr int64_t kMaxDropCols = int64_t(1) << 40;
 constexpr int64_t kMaxRows = int64_t(1) << 40;
 
 inline size_t elem_size(int dtype) { return dtype == FO_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) { return dtype == FO_BF16 || dtype == FO_FP16 || dtype == FO_F32; }
 
+inline int rows_ok(int64_t rows) {
+  return rows < 0 || rows > kMaxRows ? fail(FO_EINVAL, "rows = %lld is not in [0, 2^40]", (long long)rows) : FO_OK;
+}
 inline int shape_ok(int64_t rows, int64_t cols) {
-  if (rows < 0 || rows > kMaxRows) return fail(FO_EINVAL, "rows = %lld is not in [0, 2^40]", (long long)rows);
+  if (const int rc = rows_ok(rows)) return rc;
   if (cols < 1 || cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^26]", (long long)cols);
+  return FO_OK;
+}
+inline int drop_shape_ok(int64_t rows, int64_t cols) {
+  if (const int rc = rows_ok(rows)) return rc;
+  if (cols < 1 || cols > kMaxDropCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^40]", (long long)cols);
   return FO_OK;
 }
 

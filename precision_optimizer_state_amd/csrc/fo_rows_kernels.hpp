@@ -25,8 +25,7 @@ constexpr int BLOCK = 256;
 struct DropoutArgs {
   const void* x;
   void* y;
-  int64_t rows, x_ld;
-  int cols;
+  int64_t rows, cols, x_ld;
   DropArgs drop;
 };
 
@@ -62,23 +61,23 @@ __device__ __forceinline__ int chunks_of(int cols) { return (cols + 7) >> 3; }
 // dropout (the gradient is the same call on the output's gradient)
 // ---------------------------------------------------------------------------
 // HBM bound: 400000 x 1024 bf16 270 us, 6.1 TB/s (a copy of it without a mask runs
-// at the same rate, see DropArgs); the generator hides behind the stream.  Chunks lie one after another in memory (FLAT: packed rows of
-// whole chunks) or are found by one division, in 32 bits where the number of
-// chunks allows (Index).  Two chunks per thread, loaded before either is worked
-// on.
+// at the same rate, see DropArgs); the generator hides behind the stream.  Chunks
+// lie one after another in memory (FLAT: packed rows of whole chunks) or are found
+// by one division (Index: in 32 bits where the number of chunks and a column allow
+// it).  Two chunks per thread, loaded before either is worked on.
 constexpr int DROP_PER = 2;
 
 template <typename T, bool FLAT, typename Index>
 __global__ __launch_bounds__(BLOCK) void k_dropout(DropoutArgs a) {
   typedef typename T::raw raw;
-  const int nch = chunks_of(a.cols);
-  const Index total = (Index)(a.rows * nch);
+  const Index nch = (Index)((a.cols + 7) >> 3);
+  const Index total = (Index)(a.rows * (int64_t)nch);
   const DropKey key = drop_key(a.drop);
   const int64_t step = (int64_t)gridDim.x * (BLOCK * DROP_PER);
   for (int64_t base = (int64_t)blockIdx.x * (BLOCK * DROP_PER) + threadIdx.x; base < (int64_t)total; base += step) {
     Chunk<T> in[DROP_PER];
     int64_t at[DROP_PER];
-    int col[DROP_PER], cnt[DROP_PER];
+    int col[DROP_PER], end[DROP_PER], cnt[DROP_PER];
 #pragma unroll
     for (int v = 0; v < DROP_PER; ++v) {
       const int64_t i = base + v * BLOCK;
@@ -88,17 +87,20 @@ __global__ __launch_bounds__(BLOCK) void k_dropout(DropoutArgs a) {
         cnt[v] = live ? 8 : 0;
         in[v] = load_part<T>((const raw*)a.x + at[v], 0, cnt[v]);
       } else {
-        const Index r = live ? (Index)i / (Index)nch : 0;
-        col[v] = live ? (int)((Index)i - r * (Index)nch) * 8 : a.cols;
-        at[v] = (int64_t)r * a.cols + col[v];
-        cnt[v] = a.cols - col[v];
-        in[v] = load_part<T>((const raw*)a.x + (int64_t)r * a.x_ld, col[v], a.cols);
+        const Index r = live ? (Index)i / nch : 0, c = live ? ((Index)i - r * nch) * 8 : 0;
+        // columns of 64 bits are counted from the chunk before, as far as the chunk after
+        const int64_t from = sizeof(Index) == 8 && c > 8 ? (int64_t)c - 8 : 0, left = a.cols - from;
+        end[v] = sizeof(Index) == 8 && left > 24 ? 24 : (int)left;
+        col[v] = live ? (int)((int64_t)c - from) : end[v];
+        at[v] = (int64_t)r * a.cols + (int64_t)c;
+        cnt[v] = end[v] - col[v];
+        in[v] = load_part<T>((const raw*)a.x + (int64_t)r * a.x_ld + from, col[v], end[v]);
       }
     }
 #pragma unroll
     for (int v = 0; v < DROP_PER; ++v) {
       if (cnt[v] <= 0) continue;
-      if constexpr (!FLAT) settle_part<T>(in[v], col[v], a.cols);
+      if constexpr (!FLAT) settle_part<T>(in[v], col[v], end[v]);
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = elem<T>(in[v], j);

@@ -15,15 +15,15 @@ a function of a seed, an offset and the element's place, and is found again).
 All arithmetic runs in the HIP library (fo_dropout, fo_norm_forward,
 fo_norm_backward in include/foamd.h, which defines the formulas and the mask);
 a host extension (csrc/fo_rows_torch.cpp) marshals tensors and records the
-autograd graph.  Tensors must live
-on the current GPU; calls go to torch's current stream, allocate only through
-torch and never synchronise, so they can be captured into HIP graphs (a captured
-call refuses leaves that an eager autograd graph, still alive, has used on the
-default stream: capture with detached leaves).  Norms are over the last
-dimension.  Inputs whose rows are not consecutive elements at
-a constant distance are copied first.  Gradients of gradients and forward-mode
-derivatives are not provided, and the functions cannot be traced by make_fx or
-torch.jit.trace: such calls are refused.
+autograd graph.  Tensors must live on the current GPU; calls go to torch's
+current stream, allocate only through torch and never synchronise, so they can
+be captured into HIP graphs (a captured call refuses leaves that an eager
+autograd graph, still alive, has used on the default stream: capture with
+detached leaves).  Norms are over the last dimension, of at most 2^26 elements.
+Inputs whose rows are not consecutive elements at a constant distance are copied
+first.  Gradients of gradients and forward-mode derivatives are not provided, and
+the functions cannot be traced by make_fx or torch.jit.trace: such calls are
+refused.
 """
 
 from __future__ import annotations
