@@ -592,7 +592,12 @@ __global__ __launch_bounds__(BLOCK) void k_norm_bwd_rows_long(BwdArgs a) {
 
 // Gradients of weight and bias: workgroup (bx, by) sums 32 chunks of columns
 // over the rows r = by * 8 + lane row (mod 8 * splits) and writes one partial
-// sum per column (838 x 20000 bf16 layer norm 13.1 us).
+// sum per column (838 x 20000 bf16 layer norm 13.1 us).  The wider the rows the
+// fewer the ranges of rows, so a lane adds up LONG_TERMS rows at a time and then
+// those sums: one chain over all its rows would be rows / 8 long past 262144
+// columns (200003 equal rows of 262408: relative errors to 3.7e-4, against 5.9e-6).
+constexpr int LONG_TERMS = 64;
+
 template <typename T>
 __global__ __launch_bounds__(BLOCK) void k_norm_bwd_cols_long(BwdArgs a) {
   typedef typename T::raw raw;
@@ -602,18 +607,24 @@ __global__ __launch_bounds__(BLOCK) void k_norm_bwd_cols_long(BwdArgs a) {
   float dw[8], db[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.0f;
-  if (cnt > 0)
-    for (int64_t row = (int64_t)blockIdx.y * 8 + grp; row < a.rows; row += (int64_t)a.splits * 8) {
+  for (int64_t row = (int64_t)blockIdx.y * 8 + grp; cnt > 0 && row < a.rows;) {
+    float pw[8], pb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pw[j] = pb[j] = 0.0f;
+    for (int term = 0; term < LONG_TERMS && row < a.rows; ++term, row += (int64_t)a.splits * 8) {
       const float mean = a.rms ? 0.0f : a.mean[row], rstd = a.rstd[row];
       const Chunk<T> h = load_chunk<T>((const raw*)a.h + row * a.h_ld + c0, cnt);
       const Chunk<T> dy = load_chunk<T>((const raw*)a.dy + row * a.dy_ld + c0, cnt);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float g = elem<T>(dy, j);
-        dw[j] += g * ((elem<T>(h, j) - mean) * rstd);
-        db[j] += g;
+        pw[j] += g * ((elem<T>(h, j) - mean) * rstd);
+        pb[j] += g;
       }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) { dw[j] += pw[j]; db[j] += pb[j]; }
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) { sw[grp][lane * 8 + j] = dw[j]; sb[grp][lane * 8 + j] = db[j]; }
   __syncthreads();
