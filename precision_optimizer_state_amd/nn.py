@@ -198,15 +198,18 @@ class FlashLayerNorm(torch.nn.LayerNorm):
 
 
 class FlashRMSNorm(torch.nn.RMSNorm):
-    """torch.nn.RMSNorm over the last dimension, on rms_norm()."""
+    """torch.nn.RMSNorm over the last dimension, on rms_norm().  eps is 1e-6 if it
+    is not given, where torch's module takes None; None means here what it means
+    there, float32's epsilon for rows of any type."""
 
-    def __init__(self, normalized_shape, eps: float = 1e-6, elementwise_affine: bool = True, device=None, dtype=None):
+    def __init__(self, normalized_shape, eps: float | None = 1e-6, elementwise_affine: bool = True, device=None,
+                 dtype=None):
         super().__init__(_one_dim(normalized_shape), eps, elementwise_affine, device, dtype)
 
     def forward(self, x):
         if x.shape[-1:] != self.normalized_shape:
             raise ValueError(f"expected a last dimension of {self.normalized_shape[0]}, got shape {tuple(x.shape)}")
-        return rms_norm(x, self.weight, self.eps)
+        return rms_norm(x, self.weight, torch.finfo(torch.float32).eps if self.eps is None else self.eps)
 
 
 class FlashDropout(torch.nn.Module):
