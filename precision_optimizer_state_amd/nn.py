@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import copy
 import importlib.util
+import numbers
 import os
 import threading
 
@@ -178,7 +179,7 @@ def dropout_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.
 # modules
 # ---------------------------------------------------------------------------
 def _one_dim(normalized_shape):
-    shape = (normalized_shape,) if isinstance(normalized_shape, int) else tuple(normalized_shape)
+    shape = (normalized_shape,) if isinstance(normalized_shape, numbers.Integral) else tuple(normalized_shape)
     if len(shape) != 1:
         raise ValueError(f"norms are over the last dimension only, got normalized_shape {shape}")
     return shape

@@ -1,5 +1,6 @@
 """Construction of the norm modules, without a GPU."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -16,3 +17,9 @@ def test_eps_of_an_rms_norm(monkeypatch):
             module(x.to(dtype))
             assert seen.pop() == want and module.eps == args.get("eps", 1e-6)
             repr(module)
+
+
+@pytest.mark.parametrize("cls", [nn.FlashLayerNorm, nn.FlashRMSNorm])
+@pytest.mark.parametrize("size", [8, (8,), [8], torch.Size([8]), np.int64(8)])
+def test_sizes_as_torch_takes_them(cls, size):
+    assert cls(size).normalized_shape == (8,)
