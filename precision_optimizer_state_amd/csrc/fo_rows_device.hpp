@@ -97,20 +97,21 @@ __device__ __forceinline__ Chunk<T> load_chunk(const typename T::raw* ptr, int c
   return c;
 }
 
-// Stores of 16-bit chunks carry the nontemporal hint: nothing here is read back
-// by the kernel that writes it.  Measured on an RMS norm of 8192 x 4096 bf16:
-// 24.9 -> 20.0 us (the time of a plain copy); the hint on the loads as well took
-// it to 24.4.  A float32 chunk is two stores 32 bytes apart from the next lane's,
-// which a plain store joins in cache: layer norm backward 32768 x 2048, 150 us
-// against 160 with the hint.
-template <typename T>
+// Stores of 16-bit chunks carry the nontemporal hint unless the kernel that writes
+// them reads them back (REREAD: h in k_norm_fwd_long).  Measured on an RMS norm of
+// 8192 x 4096 bf16: 24.9 -> 20.0 us (the time of a plain copy); the hint on the
+// loads as well took it to 24.4.  What is read back loses by it: residual + layer
+// norm of 838 x 20000 bf16, 46.6 us against 41.8.  A float32 chunk is two stores 32
+// bytes apart from the next lane's, which a plain store joins in cache: layer norm
+// backward 32768 x 2048, 150 us against 160 with the hint.
+template <typename T, bool REREAD = false>
 __device__ __forceinline__ void store_chunk(typename T::raw* ptr, const Chunk<T>& c, int cnt) {
   FO_GLB typename T::raw* p = (FO_GLB typename T::raw*)ptr;
   if (cnt >= 8) {
 #pragma unroll
     for (int q = 0; q < dwords<T> / 4; ++q) {
       const v4u v = {c.w[4 * q], c.w[4 * q + 1], c.w[4 * q + 2], c.w[4 * q + 3]};
-      if constexpr (is_f32<T>) ((FO_GLB typename T::vec*)p)[q] = v;
+      if constexpr (is_f32<T> || REREAD) ((FO_GLB typename T::vec*)p)[q] = v;
       else __builtin_nontemporal_store(v, (FO_GLB typename T::vec*)p + q);
     }
     return;

@@ -497,7 +497,7 @@ __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
       if (a.residual) {
         const Chunk<T> res = load_chunk<T>((const raw*)a.residual + row * a.residual_ld + c0, cnt);
         c = join<T>(c, res, a.dropping, a.drop, key, (uint64_t)row * (uint64_t)chunks_of(a.cols) + (uint64_t)(c0 >> 3));
-        store_chunk<T>((raw*)a.h + row * a.cols + c0, c, cnt);
+        store_chunk<T, true>((raw*)a.h + row * a.cols + c0, c, cnt);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
