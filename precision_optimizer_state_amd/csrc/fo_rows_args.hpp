@@ -76,9 +76,12 @@ struct Arrays {
 struct Spread { int lanes, chunks; };
 
 // Forward: the fewest lanes that cover the row with up to two chunks each, and
-// three between 512 and 768 columns, which leaves no lane idle at 768 (8192 x 768
-// bf16 layer norm 6.1 us against 6.7 us with 64 lanes of two, with dropout and
-// residual 9.8 against 10.2).
+// three between 512 and 768 columns, where 64 lanes of two leave up to half of
+// them idle (131072 rows of 520 columns bf16, layer norm 54.1 us against 61.5, with
+// dropout and residual 111 against 119; of 640 columns 56.5 against 64.6 and 114
+// against 125; of 768, where it is a quarter, 68.9 against 69.5 and 139 against 135,
+// and at 8192 rows 6.2 against 6.4 and 10.8 against 11.1).  Float32 rows lose 5% by
+// it (RMS norm of 32768 x 640, 40.3 us against 38.1).
 inline Spread fwd_spread(int64_t cols) {
   const int64_t n = (cols + 7) / 8;
   if (n <= 8) return {8, 1};
@@ -89,9 +92,11 @@ inline Spread fwd_spread(int64_t cols) {
 }
 
 // Backward: one chunk per lane (see k_norm_bwd), two where 1024 lanes of one do
-// not reach; two of float32, or two with dropout, do not fit the registers of 1024
-// threads (1024 x 16384 bf16 layer norm, 32 us against 43 for the kernels of long
-// rows; with residual and dropout 68 against 57).
+// not reach, against the kernels of long rows, last sums included: 1024 x 16384 bf16
+// layer norm 36.4 us against 45.6, with residual (which spills 5 registers) 44.6
+// against 52.0; 1024 x 8200, 24.0 against 27.9 and 29.5 against 33.3.  Two of float32,
+// or two with dropout, do not fit the registers of 1024 threads: 1024 x 16384 bf16
+// with residual and dropout takes 67.3 us so, 58.1 with the kernels of long rows.
 inline Spread bwd_spread(int64_t cols, int dtype, bool dropping) {
   const int64_t n = (cols + 7) / 8;
   for (int lanes = 8; lanes <= 1024; lanes *= 2)

@@ -324,18 +324,19 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
 // teams of a workgroup add theirs through LDS at the end, and k_norm_bwd_reduce
 // adds the workgroups'.  One pass over h, dy and dh, HBM bound: RMS norm of 8192 x
 // 4096 bf16 34.2 us and 3.9 for the last sums, of 131072 x 768 102 us (5.9 TB/s);
-// with dh and dropout 184 us (5.5 TB/s, where arithmetic begins to show: 350
-// instructions per chunk, 20 of them the generator's quarter-rate products).
+// with dh and dropout 190-209 us from box to box (5.3-4.8 TB/s; arithmetic bounds it
+// there: 350 instructions per chunk, 20 of them the generator's quarter-rate
+// products, on lanes of which 768 columns leave a quarter idle).
 //
 // One chunk per lane and one workgroup of 16 waves on each compute unit: a second
 // chunk costs 24 registers and drops the waves to 8, and twice the workgroups
 // write twice the partial sums (8192 x 4096 bf16 RMS norm, sums included and with
 // the caches full of other data: 42.8 us; two chunks per lane 53.0, 512 workgroups
-// of half the size 52.3).  At 768 columns 128 lanes leave a quarter idle, and 32
-// lanes of three chunks are slower all the same (184 us against 197 at 131072
-// rows with dropout).  AHEAD: the next rows' loads go out before the current ones
-// are worked on (184 us against 196); two rows ahead gain nothing more.  With two
-// chunks per lane, the widest rows, registers do not allow it.
+// of half the size 52.3).  32 lanes of three chunks, which leave none idle at 768
+// columns, have no registers for it (131072 rows with dropout, last sums included,
+// 449 us against 193).  AHEAD: the next rows' loads go out before the current ones
+// are worked on (188 us against 201 in one session); two rows ahead gain nothing
+// more.  With two chunks per lane, the widest rows, registers do not allow it.
 template <typename T, int LANES, int NV, int THREADS, int MODE>
 __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
   typedef typename T::raw raw;
@@ -482,7 +483,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(BwdArgs a) {
 }
 
 // One workgroup per row, the row read once per pass (from cache after the first):
-// rows of any length.  838 x 20000 bf16 layer norm 26.8 us (2.5 TB/s).
+// rows of any length.  838 x 20000 bf16 layer norm 27.2 us (2.5 TB/s), with a
+// residual 39.8: a workgroup's 256 lanes wait for one chunk each per pass.
 template <typename T>
 __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
   __shared__ float red[BLOCK / 64];
@@ -540,7 +542,7 @@ __global__ __launch_bounds__(BLOCK) void k_norm_fwd_long(FwdArgs a) {
 }
 
 // Gradients of the rows: one workgroup per row, two passes over it (838 x 20000
-// bf16 layer norm 27.8 us).
+// bf16 layer norm 28.0 us).
 template <typename T>
 __global__ __launch_bounds__(BLOCK) void k_norm_bwd_rows_long(BwdArgs a) {
   __shared__ float red[BLOCK / 64];
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(BLOCK) void k_norm_bwd_rows_long(BwdArgs a) {
 
 // Gradients of weight and bias: workgroup (bx, by) sums 32 chunks of columns
 // over the rows r = by * 8 + lane row (mod 8 * splits) and writes one partial
-// sum per column (838 x 20000 bf16 layer norm 13.1 us).  The wider the rows the
+// sum per column (838 x 20000 bf16 layer norm 13.4 us).  The wider the rows the
 // fewer the ranges of rows, so a lane adds up LONG_TERMS rows at a time and then
 // those sums: one chain over all its rows would be rows / 8 long past 262144
 // columns (200003 equal rows of 262408: relative errors to 3.7e-4, against 5.9e-6).
