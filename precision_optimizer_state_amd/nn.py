@@ -113,6 +113,8 @@ class DropoutCounter:
                     given[drawn] = self._fresh()
                     if len(given) > self._REMEMBERED:
                         del given[next(iter(given))]
+                elif not backward and given[drawn] == (self.seed, self.offset):
+                    self._fresh()               # a program that runs again from this state
                 seed, offset = given[drawn]
         return {"seed": seed, "offset": offset, "state": self.state}
 
@@ -133,7 +135,9 @@ class DropoutCounter:
     def load_state_dict(self, sd: dict) -> None:
         if (sd["state"] is None) != (self.state is None):
             raise ValueError("one of the counters has a device state and the other has none")
-        self.seed, self.offset = int(sd["seed"]), int(sd["offset"])
+        with _lock:
+            self.seed, self.offset = int(sd["seed"]), int(sd["offset"])
+            self.__dict__.pop("_given", None)
         if self.state is not None:
             self.state.copy_(torch.tensor(sd["state"], dtype=torch.int64))
 
@@ -215,10 +219,10 @@ class FlashRMSNorm(torch.nn.RMSNorm):
 
 class FlashDropout(torch.nn.Module):
     """torch.nn.Dropout on dropout(); `counter` (shared between modules or not)
-    gives every call its mask, and a recomputed call
-    the mask of its first run.  Copies of the module share the counter, so they
-    draw masks of their own.  What resumes the masks is the counter's
-    state_dict(), saved beside the model's, which holds nothing of it."""
+    gives every call its mask, and a recomputed call the mask of its first run.
+    Copies of the module share the counter, so they draw masks of their own.
+    What resumes the masks is the counter's state_dict(), saved beside the
+    model's, which holds nothing of it."""
 
     def __init__(self, p: float, counter: DropoutCounter):
         super().__init__()

@@ -170,3 +170,31 @@ def test_copied_modules_share_the_counter_and_not_the_masks():
     other = copy.deepcopy(counter)
     other.next()
     assert counter.offset == 4 and other.offset == 5
+
+
+def test_runs_repeat_from_a_restored_counter_and_generator():
+    """The same program twice in one process, from the same state of torch's generator and of the
+    counter, in every way to set the latter: same keys, and the counter ends at the same offset."""
+    def program(counter):
+        with torch.no_grad():
+            keys = [counter.next()["offset"] for _ in range(3)]
+        x = torch.randn(9, 4, requires_grad=True)
+        checkpoint(lambda t: drop(t, counter.next()), x, use_reentrant=False).sum().backward()
+        return keys + [counter.next()["offset"], counter.offset]
+
+    counter = nn.DropoutCounter(seed=1)
+    saved = counter.state_dict()
+    torch.manual_seed(3)
+    first = program(counter)
+    assert first == [0, 1, 2, 4, 5]
+    torch.manual_seed(3)
+    counter.offset = 0
+    assert program(counter) == first
+    torch.manual_seed(3)
+    counter.load_state_dict(saved)
+    assert program(counter) == first
+    # another seed is not answered with keys of the one before
+    torch.manual_seed(3)
+    counter.load_state_dict({"seed": 2, "offset": 7, "state": None})
+    with torch.no_grad():
+        assert counter.next() == {"seed": 2, "offset": 7, "state": None}
