@@ -324,7 +324,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(FwdArgs a) {
 // teams of a workgroup add theirs through LDS at the end, and k_norm_bwd_reduce
 // adds the workgroups'.  One pass over h, dy and dh, HBM bound: RMS norm of 8192 x
 // 4096 bf16 34.2 us and 3.9 for the last sums, of 131072 x 768 102 us (5.9 TB/s);
-// with dh and dropout 190-209 us from box to box (5.3-4.8 TB/s; arithmetic bounds it
+// with dh and dropout 190-209 us from card to card (5.3-4.8 TB/s; arithmetic bounds it
 // there: 350 instructions per chunk, 20 of them the generator's quarter-rate
 // products, on lanes of which 768 columns leave a quarter idle).
 //
