@@ -28,6 +28,7 @@ refused.
 
 from __future__ import annotations
 
+import collections
 import copy
 import importlib.util
 import numbers
@@ -103,7 +104,7 @@ class DropoutCounter:
                 seed, offset = self._fresh()
             else:
                 drawn, backward = again
-                given = self.__dict__.setdefault("_given", {})
+                given = self.__dict__.setdefault("_given", collections.OrderedDict())
                 if drawn not in given:
                     if backward:
                         raise RuntimeError(
@@ -112,7 +113,7 @@ class DropoutCounter:
                             "take the arguments from next() outside the recomputed function")
                     given[drawn] = self._fresh()
                     if len(given) > self._REMEMBERED:
-                        del given[next(iter(given))]
+                        given.popitem(last=False)
                 elif not backward and given[drawn] == (self.seed, self.offset):
                     self._fresh()               # a program that runs again from this state
                 seed, offset = given[drawn]
