@@ -481,6 +481,136 @@ int fo_norm_backward(const fo_norm_bwd* args, void* stream);
  * of this size.  Host-only query.  Errors: FO_EINVAL. */
 int fo_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * Gradient clipping, linear cross entropy and the gated block: the remaining
+ * operators of a training step of the models whose weights the fused steps
+ * update.  The conventions are the row operators': any element type (`dtype`),
+ * inputs with a row stride, packed outputs that overlap nothing, float32
+ * arithmetic or wider, one rounding per output, no allocation, no
+ * synchronisation, nothing kept between calls (all may be captured), results
+ * that repeat bit for bit.  A workspace is scratch: 256-byte aligned, at least
+ * as large as the query says for the same arguments, and not shared by calls
+ * that may run at the same time.
+ * ------------------------------------------------------------------------ */
+enum fo_norm_order { FO_NORM_MAX = 0, FO_NORM_1 = 1, FO_NORM_2 = 2 };
+
+/* One gradient tensor of n elements. */
+typedef struct fo_grad {
+  const void* grad;         /* n of dtype */
+  void*       out;          /* n of out_dtype (written), may be grad itself; not read by fo_grad_norm */
+  int64_t     n;
+  int32_t     dtype, out_dtype;
+} fo_grad;
+
+/* Bytes of workspace of the two calls below, whatever the list.  Host-only
+ * query.  Errors: FO_EINVAL. */
+int fo_grad_workspace(int64_t* bytes);
+
+/*
+ * fo_grad_norm
+ * norm[0] = (sum |g|^2)^(1/2), sum |g| or max |g| (`order`) over every element
+ * of the list, summed in float64 and rounded to float32.  A NaN anywhere gives
+ * NaN, an infinity (without one) infinity.  An empty list gives 0.  Lists hold
+ * at most 2^17 tensors.  Errors: FO_EINVAL, FO_EALIAS, FO_EHIP, FO_ENOMEM.
+ */
+int fo_grad_norm(const fo_grad* list, int32_t count, int32_t order, float* norm, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+
+/*
+ * fo_grad_clip
+ * norm as above; c = min(1, max_norm / (norm + 1e-6)) (NaN if the norm is),
+ * rounded to float32; out = c * g, rounded once.  Where c is 1 a tensor whose
+ * out is its grad is left as it is.  No out may overlap another tensor's
+ * arrays: a tensor listed twice is refused (FO_EALIAS).  out == grad needs
+ * equal types.  max_norm is >= 0; infinity is no bound: c is 1 then, whatever
+ * the norm.
+ */
+int fo_grad_clip(const fo_grad* list, int32_t count, int32_t order, double max_norm, float* norm, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+
+enum fo_loss_reduction { FO_LOSS_NONE = 0, FO_LOSS_MEAN = 1, FO_LOSS_SUM = 2 };
+
+/* Arguments of the linear cross entropy.  Limits: rows 2^21, cols 2^20, vocab
+ * 2^24, rows * vocab 2^38. */
+typedef struct fo_loss {
+  const void*    x;         /* rows x cols */
+  const void*    weight;    /* vocab x cols */
+  const int64_t* target;    /* rows; in [0, vocab) or ignore_index */
+  float*         loss;      /* forward: rows, or 1 with a reduction (written) */
+  float*         lse;       /* rows: written by forward, read by backward */
+  float*         count;     /* 1: the number of counted rows; written by forward with a reduction, read by backward for the mean */
+  const float*   dloss;     /* backward: the loss's gradient, rows or 1 */
+  void*          dx;        /* backward: rows x cols (written), or NULL */
+  void*          dweight;   /* backward: vocab x cols (written), or NULL */
+  void*          workspace;
+  int64_t        workspace_bytes;
+  int64_t        rows, cols, vocab, x_ld, weight_ld, dloss_ld;  /* dloss_ld: elements between rows' dloss (FO_LOSS_NONE) */
+  int64_t        ignore_index;
+  double         smoothing; /* in [0, 1] */
+  int32_t        dtype, reduction;
+} fo_loss;
+
+/*
+ * fo_loss_forward
+ *   z = weight x (float32, never stored);  lse = log sum_v exp z_v
+ *   loss = lse - (1 - smoothing) z_target - smoothing mean_v z_v,
+ *   0 for rows whose target is ignore_index (not counted), NaN for rows whose
+ *   target is neither that nor in [0, vocab).
+ * FO_LOSS_SUM adds the rows up, FO_LOSS_MEAN divides by the counted rows'
+ * number (NaN if there are none).
+ */
+int fo_loss_forward(const fo_loss* args, void* stream);
+int fo_loss_forward_workspace(const fo_loss* args, int64_t* bytes);
+
+/*
+ * fo_loss_backward
+ *   dz = (softmax(z) - (1 - smoothing) [v = target] - smoothing / vocab) f
+ *   with f the row's dloss (mean: over the count), 0 for rows not counted
+ *   (whose x may hold anything, NaN included)
+ *   dx = dz weight;  dweight = dz^T x
+ * The logits are computed again, a piece of the vocabulary at a time; a piece's
+ * dz is rounded to dtype, f apart.  Rows with an invalid target give NaN.
+ */
+int fo_loss_backward(const fo_loss* args, void* stream);
+int fo_loss_backward_workspace(const fo_loss* args, int64_t* bytes);
+
+enum fo_activation { FO_SILU = 0, FO_GELU = 1, FO_GELU_TANH = 2 };
+
+/* Arguments of the gated block.  Limits: rows 2^21, cols and features 2^20. */
+typedef struct fo_gated {
+  const void* x;            /* rows x cols */
+  const void* gate;         /* features x cols */
+  const void* up;           /* features x cols */
+  void*       y;            /* forward: rows x features (written) */
+  float*      g;            /* rows x features: written by forward if not NULL, read by backward */
+  float*      u;            /* likewise; both or none */
+  const void* dy;           /* backward: rows x features */
+  void*       dx;           /* backward: rows x cols (written), or NULL */
+  void*       dgate;        /* backward: features x cols (written), or NULL */
+  void*       dup;          /* likewise; both or none */
+  void*       workspace;
+  int64_t     workspace_bytes;
+  int64_t     rows, cols, features, x_ld, gate_ld, up_ld, dy_ld;
+  int32_t     dtype, activation;
+} fo_gated;
+
+/*
+ * fo_gated_forward
+ *   g = gate x, u = up x (float32);  y = act(g) u
+ *   silu(g) = g / (1 + exp(-g));  gelu(g) = g Phi(g);  gelu_tanh(g) = g (1 +
+ *   tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
+ */
+int fo_gated_forward(const fo_gated* args, void* stream);
+int fo_gated_forward_workspace(const fo_gated* args, int64_t* bytes);
+
+/*
+ * fo_gated_backward
+ *   dg = dy u act'(g), du = dy act(g), both rounded to dtype
+ *   dx = dg gate + du up;  dgate = dg^T x;  dup = du^T x
+ */
+int fo_gated_backward(const fo_gated* args, void* stream);
+int fo_gated_backward_workspace(const fo_gated* args, int64_t* bytes);
+
 /* Number of launch-table cache slots pinned by calls made under HIP graph
  * capture (all devices).  Host-only query; never fails. */
 int fo_cache_pinned(void);

@@ -8,6 +8,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(PKG, "csrc", "fo_lib.hip")          # the optimizer step
 ROWS_SRC = os.path.join(PKG, "csrc", "fo_rows.hip")     # the row operators
+PRODUCTS_SRC = os.path.join(PKG, "csrc", "fo_products.hip")    # linear cross entropy, the gated block
+GRADS_SRC = os.path.join(PKG, "csrc", "fo_grads.hip")   # gradient norms and clipping
 OUT_DIR = os.path.join(PKG, "lib")
 OUT = os.path.join(OUT_DIR, "libfoamd.so")
 
@@ -30,7 +32,7 @@ def build(verbose: bool = False, extra=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     flags = [f for f in FLAGS if f != "-shared"]
     jobs = []
-    for src in (SRC, ROWS_SRC):
+    for src in (SRC, ROWS_SRC, PRODUCTS_SRC, GRADS_SRC):
         obj = os.path.join(OUT_DIR, os.path.basename(src)[:-4] + ".o")
         cmd = ["/opt/rocm/bin/hipcc", *flags, *extra, "-c", src, "-o", obj]
         if verbose:

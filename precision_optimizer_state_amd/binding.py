@@ -28,13 +28,19 @@ _STEP_EXPORTS = (
     "fo_selftest", "fo_cache_pinned", "fo_last_error", "fo_abi_version",
 )
 _ROW_EXPORTS = ("fo_dropout", "fo_norm_forward", "fo_norm_backward", "fo_norm_backward_workspace")
-EXPORTS = _STEP_EXPORTS + _ROW_EXPORTS
+_GRAD_EXPORTS = ("fo_grad_workspace", "fo_grad_norm", "fo_grad_clip")
+_PRODUCT_EXPORTS = ("fo_loss_forward", "fo_loss_forward_workspace", "fo_loss_backward", "fo_loss_backward_workspace",
+                    "fo_gated_forward", "fo_gated_forward_workspace", "fo_gated_backward", "fo_gated_backward_workspace")
+EXPORTS = _STEP_EXPORTS + _ROW_EXPORTS + _GRAD_EXPORTS + _PRODUCT_EXPORTS
 
 WFMT = {"bf16": FO_BF16, "fp16": FO_FP16}
 CODEC = {"companded": FO_COMPANDED, "linear": FO_LINEAR, "companded4": FO_COMPANDED4,
          "companded_bf16scale": FO_COMPANDED_BF16SCALE}
 KIND = {"m": FO_MOMENTUM, "v": FO_VARIANCE}
 NORM = {"layer": FO_LAYER_NORM, "rms": FO_RMS_NORM}
+FO_NORM_MAX, FO_NORM_1, FO_NORM_2 = 0, 1, 2
+REDUCTION = {"none": 0, "mean": 1, "sum": 2}
+ACTIVATION = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
 class FoError(RuntimeError):
@@ -86,6 +92,27 @@ class NormBwd(ctypes.Structure):
                 ("dtype", c_int32), ("wdtype", c_int32), ("kind", c_int32), ("reserved", c_int32)]
 
 
+class Grad(ctypes.Structure):
+    _fields_ = [("grad", c_void_p), ("out", c_void_p), ("n", c_int64), ("dtype", c_int32), ("out_dtype", c_int32)]
+
+
+class Loss(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("weight", c_void_p), ("target", c_void_p), ("loss", c_void_p), ("lse", c_void_p),
+                ("count", c_void_p), ("dloss", c_void_p), ("dx", c_void_p), ("dweight", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_int64),
+                ("rows", c_int64), ("cols", c_int64), ("vocab", c_int64), ("x_ld", c_int64), ("weight_ld", c_int64),
+                ("dloss_ld", c_int64), ("ignore_index", c_int64), ("smoothing", c_double),
+                ("dtype", c_int32), ("reduction", c_int32)]
+
+
+class Gated(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("gate", c_void_p), ("up", c_void_p), ("y", c_void_p), ("g", c_void_p),
+                ("u", c_void_p), ("dy", c_void_p), ("dx", c_void_p), ("dgate", c_void_p), ("dup", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_int64),
+                ("rows", c_int64), ("cols", c_int64), ("features", c_int64), ("x_ld", c_int64), ("gate_ld", c_int64),
+                ("up_ld", c_int64), ("dy_ld", c_int64), ("dtype", c_int32), ("activation", c_int32)]
+
+
 _lib = None
 ABI_VERSION = 6          # FO_ABI_VERSION of include/foamd.h (struct layouts below)
 
@@ -128,6 +155,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.fo_norm_backward_workspace.argtypes = [c_int64, c_int64, ctypes.POINTER(c_int64)]
         for name in _ROW_EXPORTS:
             getattr(lib, name).restype = c_int
+    if all(hasattr(lib, name) for name in _GRAD_EXPORTS + _PRODUCT_EXPORTS):
+        lib.fo_grad_workspace.argtypes = [ctypes.POINTER(c_int64)]
+        lib.fo_grad_norm.argtypes = [ctypes.POINTER(Grad), c_int32, c_int32, P, P, c_int64, P]
+        lib.fo_grad_clip.argtypes = [ctypes.POINTER(Grad), c_int32, c_int32, c_double, P, P, c_int64, P]
+        for name, args in (("loss", Loss), ("gated", Gated)):
+            for way in ("forward", "backward"):
+                getattr(lib, f"fo_{name}_{way}").argtypes = [ctypes.POINTER(args), P]
+                getattr(lib, f"fo_{name}_{way}_workspace").argtypes = [ctypes.POINTER(args), ctypes.POINTER(c_int64)]
+        for name in _GRAD_EXPORTS + _PRODUCT_EXPORTS:
+            getattr(lib, name).restype = c_int
     _lib = lib
     return lib
 
@@ -136,6 +173,15 @@ def _load_rows() -> ctypes.CDLL:
     lib = load()
     if not hasattr(lib, "fo_norm_forward"):
         raise ImportError(f"{LIB_PATH} has no row operators: rebuild it with __graft_entry__.build()")
+    return lib
+
+
+def _load_step() -> ctypes.CDLL:
+    """The library with clipping, the loss and the gated block."""
+    lib = load()
+    if not hasattr(lib, "fo_grad_clip") or not hasattr(lib, "fo_gated_backward"):
+        raise ImportError(f"{LIB_PATH} has no gradient clipping, linear cross entropy or gated block: rebuild it with "
+                          "__graft_entry__.build()")
     return lib
 
 
@@ -427,6 +473,132 @@ def fo_norm_backward(dy, h, rstd, kind="layer", mean=None, weight=None, dh=None,
                 shape[0], shape[1], dy_ld, dh_ld, h_ld, drop or _NO_DROPOUT,
                 _dtype(h), _dtype(param) if param is not None else _dtype(h), _fmt(kind, NORM), 0)
     _check(_load_rows().fo_norm_backward(ctypes.byref(a), _stream(stream)))
+
+
+def _grad_list(grads, outs):
+    rows = (Grad * max(1, len(grads)))()
+    for row, g, o in zip(rows, grads, outs):
+        if g.is_neg() or (o is not None and o.is_neg()):
+            raise ValueError("a gradient is a negated view: resolve_neg() it first")
+        if o is not None and o.numel() != g.numel():
+            raise ValueError(f"a gradient of {g.numel()} elements is clipped into {o.numel()}")
+        row.grad, row.n, row.dtype = _ptr(g), g.numel(), _dtype(g)
+        if o is not None:
+            row.out, row.out_dtype = _ptr(o), _dtype(o)
+    return rows
+
+
+def _scratch(nbytes, workspace, stream, device):
+    """(tensor, address, bytes) of a call's workspace, allocated here if none is given."""
+    import torch
+    if workspace is None:
+        if stream is not None and nbytes:   # torch would hand the memory on in its own stream's order
+            raise ValueError("a call on a stream given by hand needs a workspace of its own")
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def fo_grad_workspace() -> int:
+    out = c_int64(0)
+    _check(_load_step().fo_grad_workspace(ctypes.byref(out)))
+    return out.value
+
+
+def fo_grad_norm(grads, norm_out, order=FO_NORM_2, workspace=None, stream=None) -> None:
+    """norm_out (1 float32) = the norm of all of `grads` (contiguous tensors) together."""
+    import torch
+    grads = list(grads)
+    held, ws, nbytes = _scratch(fo_grad_workspace(), workspace, stream, norm_out.device)
+    _check(_load_step().fo_grad_norm(_grad_list(grads, [None] * len(grads)), len(grads), int(order),
+                                     _vec("norm_out", norm_out.view(-1), 1, torch.float32), ws, nbytes, _stream(stream)))
+
+
+def fo_grad_clip(grads, outs, max_norm, norm_out, order=FO_NORM_2, workspace=None, stream=None) -> None:
+    """outs[i] = c grads[i] with c = min(1, max_norm / (norm + 1e-6)); outs[i] may be grads[i]."""
+    import torch
+    grads, outs = list(grads), list(outs)
+    if len(grads) != len(outs):
+        raise ValueError(f"{len(grads)} gradients are clipped into {len(outs)} tensors")
+    held, ws, nbytes = _scratch(fo_grad_workspace(), workspace, stream, norm_out.device)
+    _check(_load_step().fo_grad_clip(_grad_list(grads, outs), len(grads), int(order), float(max_norm),
+                                     _vec("norm_out", norm_out.view(-1), 1, torch.float32), ws, nbytes, _stream(stream)))
+
+
+def _run(name, args, workspace, stream, device) -> None:
+    lib = _load_step()
+    need = c_int64(0)
+    _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
+    held, args.workspace, args.workspace_bytes = _scratch(need.value, workspace, stream, device)
+    _check(getattr(lib, name)(ctypes.byref(args), _stream(stream)))
+
+
+def _loss_args(x, weight, target, reduction, ignore_index, smoothing):
+    import torch
+    xp, x_ld = _rows_in("x", x)
+    wp, w_ld = _rows_in("weight", weight, None, x.dtype)
+    if weight.shape[1] != x.shape[1]:
+        raise ValueError(f"weight has {weight.shape[1]} columns, x {x.shape[1]}")
+    return Loss(x=xp, weight=wp, target=_vec("target", target, x.shape[0], torch.int64), rows=x.shape[0], cols=x.shape[1],
+                vocab=weight.shape[0], x_ld=x_ld, weight_ld=w_ld, ignore_index=int(ignore_index), smoothing=float(smoothing),
+                dtype=_dtype(x), reduction=_fmt(reduction, REDUCTION))
+
+
+def fo_loss_forward(x, weight, target, loss_out, lse_out, count_out=None, reduction="mean", ignore_index=-100, smoothing=0.0,
+                    workspace=None, stream=None) -> None:
+    """Softmax cross entropy of the logits x weight^T against target (int64).
+    loss_out: (rows,) or, with a reduction, (1,) float32; lse_out: (rows,);
+    count_out: (1,), with a reduction."""
+    import torch
+    a = _loss_args(x, weight, target, reduction, ignore_index, smoothing)
+    a.loss = _vec("loss_out", loss_out, x.shape[0] if a.reduction == 0 else 1, torch.float32)
+    a.lse = _vec("lse_out", lse_out, x.shape[0], torch.float32)
+    a.count = _vec("count_out", count_out, 1, torch.float32)
+    _run("fo_loss_forward", a, workspace, stream, x.device)
+
+
+def fo_loss_backward(x, weight, target, lse, dloss, count=None, dx_out=None, dweight_out=None, reduction="mean",
+                     ignore_index=-100, smoothing=0.0, workspace=None, stream=None) -> None:
+    """The gradients of fo_loss_forward; dloss: (rows,) or (1,) float32."""
+    import torch
+    a = _loss_args(x, weight, target, reduction, ignore_index, smoothing)
+    a.lse, a.count = _vec("lse", lse, x.shape[0], torch.float32), _vec("count", count, 1, torch.float32)
+    a.dloss, a.dloss_ld = _vec("dloss", dloss, x.shape[0] if a.reduction == 0 else 1, torch.float32), 1
+    a.dx = _rows_out("dx_out", dx_out, x.shape, x.dtype)
+    a.dweight = _rows_out("dweight_out", dweight_out, weight.shape, x.dtype)
+    _run("fo_loss_backward", a, workspace, stream, x.device)
+
+
+def _gated_args(x, gate, up, activation):
+    xp, x_ld = _rows_in("x", x)
+    gp, g_ld = _rows_in("gate", gate, None, x.dtype)
+    upp, u_ld = _rows_in("up", up, gate.shape, x.dtype)
+    if gate.shape[1] != x.shape[1]:
+        raise ValueError(f"the weights have {gate.shape[1]} columns, x {x.shape[1]}")
+    return Gated(x=xp, gate=gp, up=upp, rows=x.shape[0], cols=x.shape[1], features=gate.shape[0], x_ld=x_ld, gate_ld=g_ld,
+                 up_ld=u_ld, dtype=_dtype(x), activation=_fmt(activation, ACTIVATION))
+
+
+def fo_gated_forward(x, gate, up, y_out, g_out=None, u_out=None, activation="silu", workspace=None, stream=None) -> None:
+    """y_out = act(x gate^T) * (x up^T); g_out, u_out: the two products in float32."""
+    import torch
+    a = _gated_args(x, gate, up, activation)
+    shape = (x.shape[0], gate.shape[0])
+    a.y = _rows_out("y_out", y_out, shape, x.dtype)
+    a.g, a.u = _rows_out("g_out", g_out, shape, torch.float32), _rows_out("u_out", u_out, shape, torch.float32)
+    _run("fo_gated_forward", a, workspace, stream, x.device)
+
+
+def fo_gated_backward(x, gate, up, g, u, dy, dx_out=None, dgate_out=None, dup_out=None, activation="silu", workspace=None,
+                      stream=None) -> None:
+    """The gradients of fo_gated_forward, whose g_out and u_out it reads."""
+    import torch
+    a = _gated_args(x, gate, up, activation)
+    shape = (x.shape[0], gate.shape[0])
+    a.g, a.u = _rows_out("g", g, shape, torch.float32), _rows_out("u", u, shape, torch.float32)
+    a.dy, a.dy_ld = _rows_in("dy", dy, shape, x.dtype)
+    a.dx = _rows_out("dx_out", dx_out, x.shape, x.dtype)
+    a.dgate, a.dup = _rows_out("dgate_out", dgate_out, gate.shape, x.dtype), _rows_out("dup_out", dup_out, gate.shape, x.dtype)
+    _run("fo_gated_backward", a, workspace, stream, x.device)
 
 
 HBM_PROBE_MODES = {"read": 0, "write": 1, "copy": 2, "inplace": 3}

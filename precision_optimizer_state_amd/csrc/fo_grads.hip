@@ -1,0 +1,376 @@
+// fo_grads.hip -- the norm of many gradient tensors taken together, and clipping by
+// it: kernels and C ABI (see include/foamd.h for the contract).
+//
+// Both are streams over a list of tensors: the norm reads every element once; clipping
+// reads and writes them once more, and only where the norm passes the bound.  Nothing
+// is done per tensor on the host but filling a table that goes to the kernels as an
+// argument: no table is kept on the device, so calls may be captured and repeated.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "../../include/foamd.h"
+#include "fo_error.hpp"
+#include "fo_rows_args.hpp"
+#include "fo_rows_device.hpp"
+
+using namespace fo;
+using rows::Bf16;
+using rows::Fp16;
+using rows::F32;
+using rows::Chunk;
+
+namespace {
+
+#define FO_TRY(expr) do { const int rc_ = (expr); if (rc_) return rc_; } while (0)
+
+// A tensor is cut into tiles of 16384 elements; tile boundaries depend on the list
+// alone, and so do the sums' orders.
+constexpr int kBlock = 512, kPer = 8, kTile = kBlock * kPer * 4;
+// Workgroups of one call: 4 per compute unit, each of which takes consecutive tiles
+// and writes one partial sum (a launch has one at least).
+constexpr int64_t kGroups = 1024;
+constexpr int kSums = 2048;                          // partial sums that a workspace holds
+constexpr int64_t kWorkspace = kSums * (int64_t)sizeof(double);
+
+// The tensors of one launch, as its argument (which may hold 4096 bytes).
+// `first` is a tensor's first tile; `size` its elements, its types above bit 56.
+template <int N, bool OUT>
+struct Table {
+  const void* grad[N];
+  void* out[OUT ? N : 1];
+  uint64_t size[N];
+  uint32_t first[N];
+  int count;
+  uint32_t tiles;
+};
+constexpr int kInPlace = 196, kOutOfPlace = 140;
+typedef Table<kInPlace, false> Plain;
+typedef Table<kOutOfPlace, true> Paired;
+static_assert(sizeof(Plain) <= 4000 && sizeof(Paired) <= 4000, "with a launch's other arguments: 4096 bytes");
+
+constexpr uint64_t kSizeMask = (uint64_t(1) << 56) - 1;
+
+template <typename T>
+__device__ __forceinline__ void add_chunk(const Chunk<T>& c, int order, double& sum, uint32_t& top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = rows::elem<T>(c, i);
+    if (order == FO_NORM_2) sum = __builtin_fma((double)f, (double)f, sum);
+    else if (order == FO_NORM_1) sum += (double)fabsf(f);
+    else top = max(top, __float_as_uint(f) & 0x7fffffffu);      // NaN patterns are above infinity's
+  }
+}
+
+// A tile's loads are all on their way before the first is used.
+template <typename T, int ORDER>
+__device__ __forceinline__ void norm_tile(const void* grad, int64_t n, int64_t start, double& sum, uint32_t& top) {
+  const typename T::raw* p = (const typename T::raw*)grad + start;
+  const int64_t left = n - start;
+  constexpr int PASSES = kTile / (kBlock * 8);
+  Chunk<T> c[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t at = (int64_t)(i * kBlock + threadIdx.x) * 8;
+    if (at < left) c[i] = rows::load_chunk<T>(p + at, (int)min(left - at, (int64_t)8));
+    else
+#pragma unroll
+      for (int k = 0; k < rows::dwords<T>; ++k) c[i].w[k] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) add_chunk<T>(c[i], ORDER, sum, top);
+}
+
+__device__ __forceinline__ double joined(double a, double b, int order) {
+  if (order != FO_NORM_MAX) return a + b;
+  const uint32_t x = __float_as_uint((float)a), y = __float_as_uint((float)b);       // both are floats >= 0 or NaN
+  return (double)__uint_as_float(max(x & 0x7fffffffu, y & 0x7fffffffu));
+}
+
+// The sum over the workgroup, in lane 0 of wave 0 (every lane with `all`).
+__device__ __forceinline__ double block_sum(double v, int order, double* lds) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = joined(v, __shfl_xor(v, d), order);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = lds[0];
+#pragma unroll
+  for (int i = 1; i < kBlock / 64; ++i) v = joined(v, lds[i], order);
+  return v;
+}
+
+// The tensor of a tile: the last whose first tile is not past it.
+template <typename Tab>
+__device__ __forceinline__ int tensor_of(const Tab& t, uint32_t tile) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int ORDER>
+__global__ __launch_bounds__(kBlock) void k_grad_norm(Plain t, double* sums) {
+  __shared__ double lds[kBlock / 64];
+  const uint32_t begin = (uint32_t)((uint64_t)t.tiles * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)((uint64_t)t.tiles * (blockIdx.x + 1) / gridDim.x);
+  double sum = 0.0;
+  uint32_t top = 0;
+  int i = tensor_of(t, begin);
+  for (uint32_t tile = begin; tile < end; ++tile) {
+    while (i + 1 < t.count && t.first[i + 1] <= tile) ++i;
+    const int64_t n = (int64_t)(t.size[i] & kSizeMask), start = (int64_t)(tile - t.first[i]) * kTile;
+    const int dtype = (int)(t.size[i] >> 56) & 3;
+    if (dtype == FO_BF16) norm_tile<Bf16, ORDER>(t.grad[i], n, start, sum, top);
+    else if (dtype == FO_FP16) norm_tile<Fp16, ORDER>(t.grad[i], n, start, sum, top);
+    else norm_tile<F32, ORDER>(t.grad[i], n, start, sum, top);
+  }
+  if (ORDER == FO_NORM_MAX) sum = (double)__uint_as_float(top);
+  sum = block_sum(sum, ORDER, lds);
+  if (threadIdx.x == 0) ((FO_GLB double*)sums)[blockIdx.x] = sum;
+}
+
+// The norm from the partial sums, the same in every lane of every workgroup.
+__device__ __forceinline__ double whole_norm(const double* sums, int count, int order, double* lds) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < count; i += kBlock) v = joined(v, ((const FO_GLB double*)sums)[i], order);
+  v = block_sum(v, order, lds);
+  return order == FO_NORM_2 ? sqrt(v) : v;
+}
+
+__global__ __launch_bounds__(kBlock) void k_grad_norm_join(const double* sums, int count, int order, float* norm) {
+  __shared__ double lds[kBlock / 64];
+  const double v = whole_norm(sums, count, order, lds);
+  if (threadIdx.x == 0) *(FO_GLB float*)norm = (float)v;
+}
+
+template <typename T, typename O>
+__device__ __forceinline__ void clip_tile(const void* grad, void* out, int64_t n, int64_t start, float c) {
+  const typename T::raw* p = (const typename T::raw*)grad + start;
+  typename O::raw* o = (typename O::raw*)out + start;
+  const int64_t left = n - start;
+  constexpr int PASSES = kTile / (kBlock * 8);
+  Chunk<T> in[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t at = (int64_t)(i * kBlock + threadIdx.x) * 8;
+    if (at < left) in[i] = rows::load_chunk<T>(p + at, (int)min(left - at, (int64_t)8));
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t at = (int64_t)(i * kBlock + threadIdx.x) * 8;
+    if (at >= left) continue;
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = rows::elem<T>(in[i], k) * c;
+    rows::store_chunk<O>(o + at, rows::to_chunk<O>(f), (int)min(left - at, (int64_t)8));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_to(const void* grad, void* out, int out_dtype, int64_t n, int64_t start, float c) {
+  if (out_dtype == FO_BF16) clip_tile<T, Bf16>(grad, out, n, start, c);
+  else if (out_dtype == FO_FP16) clip_tile<T, Fp16>(grad, out, n, start, c);
+  else clip_tile<T, F32>(grad, out, n, start, c);
+}
+
+struct ClipArgs { const double* sums; float* norm; double max_norm; int count, order, first; };
+
+// Every workgroup joins the partial sums for itself (8 KB from L2: a launch less, and
+// no workgroup waits for another).  Tiles go from the last to the first: what the norm
+// read last is still in the memory-side cache.
+template <typename Tab, bool OUT>
+__global__ __launch_bounds__(kBlock) void k_grad_clip(Tab t, ClipArgs a) {
+  __shared__ double lds[kBlock / 64];
+  const double norm = whole_norm(a.sums, a.count, a.order, lds);
+  if (a.first && blockIdx.x == 0 && threadIdx.x == 0) *(FO_GLB float*)a.norm = (float)norm;
+  double q = a.max_norm / (norm + 1e-6);
+  if (isinf(a.max_norm) || q > 1.0) q = 1.0;
+  const float c = (float)q;
+  if (!OUT && c == 1.0f) return;
+  const uint32_t begin = (uint32_t)((uint64_t)t.tiles * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)((uint64_t)t.tiles * (blockIdx.x + 1) / gridDim.x);
+  if (begin == end) return;
+  int i = tensor_of(t, end - 1);
+  for (uint32_t tile = end; tile-- > begin;) {
+    while (t.first[i] > tile) --i;
+    const int64_t n = (int64_t)(t.size[i] & kSizeMask), start = (int64_t)(tile - t.first[i]) * kTile;
+    const int dtype = (int)(t.size[i] >> 56) & 3;
+    if constexpr (OUT) {
+      const int od = (int)(t.size[i] >> 58) & 3;
+      if (dtype == FO_BF16) clip_to<Bf16>(t.grad[i], t.out[i], od, n, start, c);
+      else if (dtype == FO_FP16) clip_to<Fp16>(t.grad[i], t.out[i], od, n, start, c);
+      else clip_to<F32>(t.grad[i], t.out[i], od, n, start, c);
+    } else {
+      void* g = const_cast<void*>(t.grad[i]);
+      if (dtype == FO_BF16) clip_tile<Bf16, Bf16>(g, g, n, start, c);
+      else if (dtype == FO_FP16) clip_tile<Fp16, Fp16>(g, g, n, start, c);
+      else clip_tile<F32, F32>(g, g, n, start, c);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+constexpr int32_t kMaxTensors = 1 << 17;
+constexpr int64_t kMaxElems = int64_t(1) << 40;      // of one tensor
+
+struct Span { uintptr_t lo, hi; bool out; };
+
+int grad_checks(const fo_grad* list, int32_t count, int32_t order, const float* norm, const void* workspace, int64_t bytes,
+                bool clip, int64_t* total) {
+  if (count < 0 || count > kMaxTensors) return fail(FO_EINVAL, "count = %d is not in [0, 2^17]", (int)count);
+  if (count && !list) return fail(FO_EINVAL, "list is NULL");
+  if (order < FO_NORM_MAX || order > FO_NORM_2) return fail(FO_EINVAL, "bad norm order %d", (int)order);
+  if (!norm || reinterpret_cast<uintptr_t>(norm) % 4) return fail(FO_EINVAL, "norm is NULL or not 4-byte aligned");
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || bytes < kWorkspace)
+    return fail(FO_EINVAL, "the workspace must be 256-byte aligned and hold %lld bytes", (long long)kWorkspace);
+  std::vector<Span> spans;
+  spans.reserve(2 * (size_t)count + 2);
+  auto add = [&](const void* p, int64_t n, bool out) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if ((uint64_t)n > UINTPTR_MAX - a) return false;
+    spans.push_back({a, a + (uintptr_t)n, out});
+    return true;
+  };
+  add(norm, 4, true);
+  add(workspace, kWorkspace, true);
+  *total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const fo_grad& t = list[i];
+    if (t.n < 0 || t.n > kMaxElems) return fail(FO_EINVAL, "tensor %d: n = %lld is not in [0, 2^40]", i, (long long)t.n);
+    if (!rows::dtype_ok(t.dtype) || (clip && !rows::dtype_ok(t.out_dtype))) return fail(FO_EINVAL, "tensor %d: bad element type", i);
+    if (t.n == 0) continue;
+    const size_t es = rows::elem_size(t.dtype);
+    if (!t.grad || reinterpret_cast<uintptr_t>(t.grad) % es) return fail(FO_EINVAL, "tensor %d: grad is NULL or misaligned", i);
+    bool fits;
+    if (clip) {
+      const size_t os = rows::elem_size(t.out_dtype);
+      if (!t.out || reinterpret_cast<uintptr_t>(t.out) % os) return fail(FO_EINVAL, "tensor %d: out is NULL or misaligned", i);
+      if (t.out == t.grad) {
+        if (t.dtype != t.out_dtype) return fail(FO_EINVAL, "tensor %d: clipped in place into another type", i);
+        fits = add(t.grad, t.n * (int64_t)es, true);
+      } else {
+        fits = add(t.grad, t.n * (int64_t)es, false) && add(t.out, t.n * (int64_t)os, true);
+      }
+    } else {
+      fits = add(t.grad, t.n * (int64_t)es, false);
+    }
+    if (!fits) return fail(FO_EINVAL, "tensor %d does not fit the address space", i);
+    *total += (t.n + kTile - 1) / kTile;
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t hi_any = 0, hi_out = 0;
+  for (const Span& s : spans) {
+    if (s.lo < hi_out || (s.out && s.lo < hi_any)) return fail(FO_EALIAS, "arrays of the list overlap at %p", (void*)s.lo);
+    hi_any = std::max(hi_any, s.hi);
+    if (s.out) hi_out = std::max(hi_out, s.hi);
+  }
+  if (*total >> 31) return fail(FO_EINVAL, "the list holds more than 2^45 elements");
+  return FO_OK;
+}
+
+int launch_check(const char* what) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? FO_OK : fail(FO_EHIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+// Launches of at most N tensors each (those that `take` accepts), with their share of
+// the workgroups.
+template <int N, bool OUT, typename Take, typename Launch>
+void each_table(const fo_grad* list, int32_t count, int64_t total, Take&& take, Launch&& launch) {
+  Table<N, OUT> t;
+  t.count = 0;
+  t.tiles = 0;
+  auto flush = [&] {
+    if (!t.count) return;
+    const int64_t share = (kGroups * t.tiles + total - 1) / total;
+    launch(t, (unsigned)std::max<int64_t>(1, std::min<int64_t>(share, t.tiles)));
+    t.count = 0;
+    t.tiles = 0;
+  };
+  for (int32_t i = 0; i < count; ++i) {
+    const fo_grad& g = list[i];
+    if (g.n == 0 || !take(g)) continue;
+    t.grad[t.count] = g.grad;
+    if (OUT) t.out[t.count] = g.out;
+    t.size[t.count] = (uint64_t)g.n | (uint64_t)g.dtype << 56 | (OUT ? (uint64_t)g.out_dtype << 58 : 0);
+    t.first[t.count] = t.tiles;
+    t.tiles += (uint32_t)((g.n + kTile - 1) / kTile);
+    if (++t.count == N) flush();
+  }
+  flush();
+}
+
+// Partial sums of the list; their number.
+int norm_launches(const fo_grad* list, int32_t count, int32_t order, int64_t total, double* sums, hipStream_t s) {
+  int n = 0;
+  each_table<kInPlace, false>(list, count, total, [](const fo_grad&) { return true; }, [&](const Plain& t, unsigned groups) {
+    if (order == FO_NORM_2) hipLaunchKernelGGL(k_grad_norm<FO_NORM_2>, groups, kBlock, 0, s, t, sums + n);
+    else if (order == FO_NORM_1) hipLaunchKernelGGL(k_grad_norm<FO_NORM_1>, groups, kBlock, 0, s, t, sums + n);
+    else hipLaunchKernelGGL(k_grad_norm<FO_NORM_MAX>, groups, kBlock, 0, s, t, sums + n);
+    n += (int)groups;
+  });
+  return n;
+}
+// a launch has at most its share, rounded up, so all have at most kGroups + one each
+static_assert(kGroups + kMaxTensors / kInPlace + 1 <= kSums, "the workspace holds every partial sum");
+
+}  // namespace
+
+extern "C" {
+
+int fo_grad_workspace(int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
+  *bytes = kWorkspace;
+  return FO_OK;
+}
+
+int fo_grad_norm(const fo_grad* list, int32_t count, int32_t order, float* norm, void* workspace, int64_t workspace_bytes,
+                 void* stream) try {
+  clear_error();
+  int64_t total = 0;
+  FO_TRY(grad_checks(list, count, order, norm, workspace, workspace_bytes, false, &total));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  double* sums = static_cast<double*>(workspace);
+  const int n = norm_launches(list, count, order, total, sums, s);
+  hipLaunchKernelGGL(k_grad_norm_join, 1, kBlock, 0, s, (const double*)sums, n, (int)order, norm);
+  return launch_check("gradient norm launch");
+} catch (const std::bad_alloc&) {
+  return fail(FO_ENOMEM, "no host memory");
+}
+
+int fo_grad_clip(const fo_grad* list, int32_t count, int32_t order, double max_norm, float* norm, void* workspace,
+                 int64_t workspace_bytes, void* stream) try {
+  clear_error();
+  if (!(max_norm >= 0.0)) return fail(FO_EINVAL, "max_norm must be >= 0");
+  int64_t total = 0;
+  FO_TRY(grad_checks(list, count, order, norm, workspace, workspace_bytes, true, &total));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  double* sums = static_cast<double*>(workspace);
+  const int n = norm_launches(list, count, order, total, sums, s);
+  ClipArgs a = {sums, norm, max_norm, n, (int)order, 1};
+  each_table<kInPlace, false>(list, count, total, [](const fo_grad& g) { return g.out == g.grad; },
+                              [&](const Plain& t, unsigned groups) {
+    hipLaunchKernelGGL((k_grad_clip<Plain, false>), groups, kBlock, 0, s, t, a);
+    a.first = 0;
+  });
+  each_table<kOutOfPlace, true>(list, count, total, [](const fo_grad& g) { return g.out != g.grad; },
+                                [&](const Paired& t, unsigned groups) {
+    hipLaunchKernelGGL((k_grad_clip<Paired, true>), groups, kBlock, 0, s, t, a);
+    a.first = 0;
+  });
+  if (a.first) hipLaunchKernelGGL(k_grad_norm_join, 1, kBlock, 0, s, (const double*)sums, n, (int)order, norm);
+  return launch_check("gradient clipping launch");
+} catch (const std::bad_alloc&) {
+  return fail(FO_ENOMEM, "no host memory");
+}
+
+}  // extern "C"

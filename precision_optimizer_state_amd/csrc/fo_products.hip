@@ -1,0 +1,387 @@
+// fo_products.hip -- C ABI of the operators built on matrix products: linear cross
+// entropy and the gated block (see include/foamd.h for the contract of every entry
+// point).  Host work is argument validation and launches; nothing here allocates,
+// synchronises, keeps state between calls or throws.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/foamd.h"
+#include "fo_error.hpp"
+#include "fo_products_args.hpp"
+#include "fo_products_kernels.hpp"
+
+using namespace fo;
+using namespace fo::prod;
+using rows::Arrays;
+
+namespace {
+
+#define FO_TRY(expr) do { const int rc_ = (expr); if (rc_) return rc_; } while (0)
+
+int launch_check(const char* what) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? FO_OK : fail(FO_EHIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+unsigned grid_of(int64_t want, int64_t most = 1 << 16) { return (unsigned)std::max<int64_t>(1, std::min(want, most)); }
+
+template <typename T, typename E, int WR, int WC, int FR, int FC, int NS>
+void launch_tile(const Product& p, const typename E::Args& e, hipStream_t s) {
+  const unsigned groups = (unsigned)p.tiles_r * (unsigned)p.tiles_c * (unsigned)p.slices;
+  hipLaunchKernelGGL((k_product<T, WR, WC, FR, FC, NS, E>), groups, WR * WC * 64, 0, s, p, e);
+}
+
+template <typename T, typename E, bool NARROW_OK>
+void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStream_t s) {
+  p.tiles_r = c.tiles_r; p.tiles_c = c.tiles_c; p.slices = c.slices;
+  if constexpr (NARROW_OK)
+    if (c.kind == NARROW) return launch_tile<T, E, 2, 1, 2, 1, 4>(p, e, s);
+  if (c.kind == WIDE) return launch_tile<T, E, 2, 4, 4, 2, 2>(p, e, s);
+  launch_tile<T, E, 2, 2, 2, 2, 2>(p, e, s);
+}
+
+uint8_t* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : static_cast<uint8_t*>(workspace) + offset; }
+
+void pack(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, hipStream_t s) {
+  const LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)rows, nullptr, 0};
+  const unsigned groups = grid_of((rows * dst_ld + 1023) / 1024);
+  if (dtype == FO_F32) hipLaunchKernelGGL(k_pack<uint32_t>, groups, 256, 0, s, a);
+  else hipLaunchKernelGGL(k_pack<uint16_t>, groups, 256, 0, s, a);
+}
+
+// dst: cols rows of dst_ld elements
+void transpose(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, int64_t width,
+               const int64_t* target, int64_t ignore, hipStream_t s) {
+  LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)width, target, ignore};
+  const unsigned groups = grid_of(((width + 63) / 64) * ((cols + 63) / 64));
+  if (dtype == FO_F32) hipLaunchKernelGGL(k_transpose<uint32_t>, groups, 256, 0, s, a);
+  else hipLaunchKernelGGL(k_transpose<uint16_t>, groups, 256, 0, s, a);
+}
+
+Product product_of(const void* r, int64_t r_ld, int64_t nr, const void* c, int64_t c_ld, int64_t nc, int64_t k, int64_t es) {
+  Product p = {};
+  p.r = r; p.c = c;
+  p.r_ld = r_ld * es; p.c_ld = c_ld * es;
+  p.nr = (int)nr; p.nc = (int)nc;
+  p.steps = (int)(k * es / 128);
+  return p;
+}
+
+// ---------------------------------------------------------------------------
+// linear cross entropy
+// ---------------------------------------------------------------------------
+int loss_checks(const fo_loss* a) {
+  if (!a) return fail(FO_EINVAL, "args is NULL");
+  if (!dtype_ok(a->dtype)) return fail(FO_EINVAL, "bad element type %d", a->dtype);
+  if (a->reduction < FO_LOSS_NONE || a->reduction > FO_LOSS_SUM) return fail(FO_EINVAL, "bad reduction %d", a->reduction);
+  if (a->rows < 0 || a->rows > kMaxTokens) return fail(FO_EINVAL, "rows = %lld is not in [0, 2^21]", (long long)a->rows);
+  if (a->cols < 1 || a->cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^20]", (long long)a->cols);
+  if (a->vocab < 1 || a->vocab > kMaxVocab) return fail(FO_EINVAL, "vocab = %lld is not in [1, 2^24]", (long long)a->vocab);
+  if (a->rows * a->vocab > kMaxLogits) return fail(FO_EINVAL, "rows * vocab is more than 2^38");
+  if (!(a->smoothing >= 0.0 && a->smoothing <= 1.0)) return fail(FO_EINVAL, "the smoothing must lie in [0, 1]");
+  return FO_OK;
+}
+
+int loss_inputs(const fo_loss* a, Arrays& ar) {
+  const size_t es = elem_size(a->dtype);
+  const bool any = a->rows > 0;
+  FO_TRY(ar.add(a->x, "x", false, any, a->rows, a->cols, a->x_ld, es));
+  FO_TRY(ar.add(a->weight, "weight", false, any, a->vocab, a->cols, a->weight_ld, es));
+  FO_TRY(ar.add(a->target, "target", false, any, a->rows, 1, 1, 8));
+  return FO_OK;
+}
+
+int workspace_check(void* workspace, int64_t have, int64_t need, Arrays& ar) {
+  if (!need) return FO_OK;
+  if (have < need)
+    return fail(FO_EINVAL, "the workspace holds %lld bytes, %lld are needed", (long long)have, (long long)need);
+  return ar.add(workspace, "workspace", true, true, 1, need, 0, 1, 256);
+}
+
+template <typename T>
+int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
+  const int64_t es = elem_bytes<T>;
+  const void *x = a->x, *w = a->weight;
+  int64_t x_ld = a->x_ld, w_ld = a->weight_ld;
+  if (f.x >= 0) { pack(a->dtype, x, x_ld, a->rows, a->cols, at(a->workspace, f.x), f.k, s); x = at(a->workspace, f.x); x_ld = f.k; }
+  if (f.w >= 0) { pack(a->dtype, w, w_ld, a->vocab, a->cols, at(a->workspace, f.w), f.k, s); w = at(a->workspace, f.w); w_ld = f.k; }
+  const bool reduced = a->reduction != FO_LOSS_NONE;
+  v2f* part = (v2f*)at(a->workspace, f.part);
+  float* sums = (float*)at(a->workspace, f.sums);
+  float* chosen = (float*)at(a->workspace, f.chosen);
+  float* each = reduced ? (float*)at(a->workspace, f.each) : a->loss;
+  const Product p = product_of(w, w_ld, a->vocab, x, x_ld, a->rows, f.k, es);
+  launch_product<T, Statistics, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
+  const LossRows r = {part, sums, chosen, a->target, each, a->lse, a->ignore_index, (int)a->rows, 2 * f.c.tiles_r,
+                      (int)a->vocab, (float)a->smoothing};
+  hipLaunchKernelGGL(k_loss_rows, (unsigned)((a->rows + 63) / 64), 1024, 0, s, r);
+  if (reduced)
+    hipLaunchKernelGGL(k_loss_sum, 1, 1024, 0, s, (const float*)each, a->target, a->ignore_index, (int)a->rows,
+                       (int)(a->reduction == FO_LOSS_MEAN), a->loss, a->count);
+  return launch_check("loss forward launch");
+}
+
+template <typename T>
+int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
+  const int64_t es = elem_bytes<T>;
+  void* ws = a->workspace;
+  float *f = (float*)at(ws, b.f), *unit = (float*)at(ws, b.unit), *factor = (float*)at(ws, b.factor);
+  const bool none = a->reduction == FO_LOSS_NONE;
+  hipLaunchKernelGGL(k_loss_factors, 1, 1024, 0, s, a->dloss, none ? a->dloss_ld : (int64_t)0,
+                     a->reduction == FO_LOSS_MEAN ? (const float*)a->count : (const float*)nullptr, a->target, a->ignore_index,
+                     (int)a->rows, f, unit, factor);
+  const void* x = a->x;
+  int64_t x_ld = a->x_ld;
+  if (b.x >= 0) { pack(a->dtype, x, x_ld, a->rows, a->cols, at(ws, b.x), b.k, s); x = at(ws, b.x); x_ld = b.k; }
+  if (a->dweight) transpose(a->dtype, a->x, a->x_ld, a->rows, a->cols, at(ws, b.xt), b.n, b.n, a->target, a->ignore_index, s);
+  // half precision holds gradients of logits times 2^15
+  const float scale = __is_same(T, Fp16) ? 32768.0f : 1.0f;
+  const int64_t slice = a->rows * b.sums_ld;
+  for (int64_t first = 0; first < a->vocab; first += b.piece) {
+    const int64_t nv = std::min(b.piece, a->vocab - first), nvp = padded(nv);
+    const uint8_t* w_at = static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es;
+    const void* w = w_at;
+    int64_t w_ld = a->weight_ld;
+    if (b.w >= 0) { pack(a->dtype, w, w_ld, nv, a->cols, at(ws, b.w), b.k, s); w = at(ws, b.w); w_ld = b.k; }
+    const Product pz = product_of(w, w_ld, nv, x, x_ld, a->rows, b.k, es);
+    // tokens in whole steps: the padding is written too (as zeros)
+    const Cut cz = cut(nv, b.n, pz.steps, false, false, false);
+    launch_product<T, LogitGradients, false>(
+        pz, cz, {at(ws, b.by_token), at(ws, b.by_place), nvp, b.n, a->lse, unit, a->target, a->ignore_index, (int)first,
+                 (int)a->vocab, scale, (float)a->smoothing}, s);
+    if (a->dx) {
+      transpose(a->dtype, w_at, a->weight_ld, nv, a->cols, at(ws, b.wt), nvp, nvp, nullptr, 0, s);
+      const Product px = product_of(at(ws, b.wt), nvp, a->cols, at(ws, b.by_token), nvp, a->rows, nvp, es);
+      Cut cx = cut(a->cols, a->rows, px.steps, false, true, false);
+      cx.slices = b.slices;
+      launch_product<T, KeepSums, true>(px, cx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
+    }
+    if (a->dweight) {
+      const Product pw = product_of(at(ws, b.xt), b.n, a->cols, at(ws, b.by_place), b.n, nv, b.n, es);
+      const Cut cw = cut(a->cols, nv, pw.steps, false, true, false);
+      launch_product<T, StoreScaled, true>(
+          pw, cw, {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
+                   1.0f / scale}, s);
+    }
+  }
+  if (a->dx) {
+    const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.slices, a->dx, f, a->target, a->ignore_index,
+                        (int)a->rows, (int)a->cols, 1.0f / scale};
+    hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
+  }
+  return launch_check("loss backward launch");
+}
+
+// ---------------------------------------------------------------------------
+// the gated block
+// ---------------------------------------------------------------------------
+int gated_checks(const fo_gated* a) {
+  if (!a) return fail(FO_EINVAL, "args is NULL");
+  if (!dtype_ok(a->dtype)) return fail(FO_EINVAL, "bad element type %d", a->dtype);
+  if (a->activation < FO_SILU || a->activation > FO_GELU_TANH) return fail(FO_EINVAL, "bad activation %d", a->activation);
+  if (a->rows < 0 || a->rows > kMaxTokens) return fail(FO_EINVAL, "rows = %lld is not in [0, 2^21]", (long long)a->rows);
+  if (a->cols < 1 || a->cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^20]", (long long)a->cols);
+  if (a->features < 1 || a->features > kMaxFeatures)
+    return fail(FO_EINVAL, "features = %lld is not in [1, 2^20]", (long long)a->features);
+  if (!a->g != !a->u) return fail(FO_EINVAL, "g and u go together");
+  return FO_OK;
+}
+
+int gated_inputs(const fo_gated* a, Arrays& ar, bool backward) {
+  const size_t es = elem_size(a->dtype);
+  const bool any = a->rows > 0;
+  FO_TRY(ar.add(a->x, "x", false, any, a->rows, a->cols, a->x_ld, es));
+  FO_TRY(ar.add(a->gate, "gate", false, any, a->features, a->cols, a->gate_ld, es));
+  FO_TRY(ar.add(a->up, "up", false, any, a->features, a->cols, a->up_ld, es));
+  FO_TRY(ar.add(a->g, "g", !backward, any && backward, a->rows, a->features, a->features, 4));
+  FO_TRY(ar.add(a->u, "u", !backward, any && backward, a->rows, a->features, a->features, 4));
+  return FO_OK;
+}
+
+template <typename T>
+int run_gated_forward(const fo_gated* a, const GatedForward& f, hipStream_t s) {
+  const int64_t es = elem_bytes<T>;
+  void* ws = a->workspace;
+  const void *x = a->x, *gate = a->gate, *up_w = a->up;
+  int64_t x_ld = a->x_ld, w_ld = a->gate_ld;
+  if (f.x >= 0) { pack(a->dtype, x, x_ld, a->rows, a->cols, at(ws, f.x), f.k, s); x = at(ws, f.x); x_ld = f.k; }
+  if (f.gate >= 0) {
+    pack(a->dtype, gate, a->gate_ld, a->features, a->cols, at(ws, f.gate), f.k, s);
+    pack(a->dtype, up_w, a->up_ld, a->features, a->cols, at(ws, f.up), f.k, s);
+    gate = at(ws, f.gate); up_w = at(ws, f.up); w_ld = f.k;
+  }
+  Product p = product_of(gate, w_ld, a->features, x, x_ld, a->rows, f.k, es);
+  p.r2 = up_w;
+  launch_product<T, Gated, true>(p, f.c, {a->y, a->g, a->u, a->activation}, s);
+  return launch_check("gated forward launch");
+}
+
+template <typename T>
+int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s) {
+  const int64_t es = elem_bytes<T>, half = b.half;
+  void* ws = a->workspace;
+  const GatedBwd g = {a->dy, a->dy_ld, a->g, a->u, at(ws, b.by_token), 2 * half, at(ws, b.by_feature), b.n,
+                      (int)a->rows, (int)a->features, (int)half, a->activation};
+  hipLaunchKernelGGL((k_gated_bwd<T>), grid_of((b.n / 64) * (half / 64)), 256, 0, s, g);
+  if (a->dx) {
+    uint8_t* wt = at(ws, b.wt);
+    transpose(a->dtype, a->gate, a->gate_ld, a->features, a->cols, wt, 2 * half, half, nullptr, 0, s);
+    transpose(a->dtype, a->up, a->up_ld, a->features, a->cols, wt + half * es, 2 * half, half, nullptr, 0, s);
+    const Product p = product_of(wt, 2 * half, a->cols, at(ws, b.by_token), 2 * half, a->rows, 2 * half, es);
+    if (b.c_dx.slices > 1) {
+      const int64_t slice = a->rows * b.sums_ld;
+      launch_product<T, KeepSums, true>(p, b.c_dx, {(float*)at(ws, b.sums), b.sums_ld, slice, 0}, s);
+      const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.c_dx.slices, a->dx, nullptr, nullptr, 0,
+                          (int)a->rows, (int)a->cols, 1.0f};
+      hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
+    } else {
+      launch_product<T, StoreScaled, true>(p, b.c_dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, nullptr, 1.0f}, s);
+    }
+  }
+  if (a->dgate || a->dup) {
+    transpose(a->dtype, a->x, a->x_ld, a->rows, a->cols, at(ws, b.xt), b.n, b.n, nullptr, 0, s);
+    const Product p = product_of(at(ws, b.xt), b.n, a->cols, at(ws, b.by_feature), b.n, 2 * half, b.n, es);
+    const Cut c = cut(a->cols, 2 * half, p.steps, false, true, false);
+    launch_product<T, StoreScaled, true>(
+        p, c, {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, nullptr, 1.0f}, s);
+  }
+  return launch_check("gated backward launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+int fo_loss_forward_workspace(const fo_loss* a, int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
+  FO_TRY(loss_checks(a));
+  *bytes = a->rows ? loss_forward(a).bytes : 0;
+  return FO_OK;
+}
+
+int fo_loss_forward(const fo_loss* a, void* stream) {
+  clear_error();
+  FO_TRY(loss_checks(a));
+  const bool any = a->rows > 0, reduced = a->reduction != FO_LOSS_NONE;
+  Arrays ar;
+  FO_TRY(loss_inputs(a, ar));
+  FO_TRY(ar.add(a->loss, "loss", true, any || reduced, reduced ? 1 : a->rows, 1, 1, 4));
+  FO_TRY(ar.add(a->lse, "lse", true, any, a->rows, 1, 1, 4));
+  FO_TRY(ar.add(a->count, "count", true, reduced, 1, 1, 1, 4));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!any) {
+    FO_TRY(ar.disjoint());
+    if (reduced)
+      hipLaunchKernelGGL(k_loss_sum, 1, 1024, 0, s, (const float*)nullptr, a->target, a->ignore_index, 0,
+                         (int)(a->reduction == FO_LOSS_MEAN), a->loss, a->count);
+    return launch_check("loss forward launch");
+  }
+  const LossForward f = loss_forward(a);
+  FO_TRY(workspace_check(a->workspace, a->workspace_bytes, f.bytes, ar));
+  FO_TRY(ar.disjoint());
+  if (a->dtype == FO_BF16) return run_loss_forward<Bf16>(a, f, s);
+  if (a->dtype == FO_FP16) return run_loss_forward<Fp16>(a, f, s);
+  return run_loss_forward<F32>(a, f, s);
+}
+
+int fo_loss_backward_workspace(const fo_loss* a, int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
+  FO_TRY(loss_checks(a));
+  *bytes = a->rows ? loss_backward(a, a->dx, a->dweight).bytes : 0;
+  return FO_OK;
+}
+
+int fo_loss_backward(const fo_loss* a, void* stream) {
+  clear_error();
+  FO_TRY(loss_checks(a));
+  const size_t es = elem_size(a->dtype);
+  const bool any = a->rows > 0, none = a->reduction == FO_LOSS_NONE;
+  Arrays ar;
+  FO_TRY(loss_inputs(a, ar));
+  FO_TRY(ar.add(a->lse, "lse", false, any, a->rows, 1, 1, 4));
+  FO_TRY(ar.add(a->count, "count", false, a->reduction == FO_LOSS_MEAN && any, 1, 1, 1, 4));
+  FO_TRY(ar.add(a->dloss, "dloss", false, any, none ? a->rows : 1, 1, none ? a->dloss_ld : 1, 4));
+  FO_TRY(ar.add(a->dx, "dx", true, false, a->rows, a->cols, a->cols, es));
+  FO_TRY(ar.add(a->dweight, "dweight", true, false, a->vocab, a->cols, a->cols, es));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!any) {
+    FO_TRY(ar.disjoint());
+    if (a->dweight) {
+      const int64_t words = a->vocab * a->cols;
+      hipLaunchKernelGGL(k_zero, grid_of((words * (int64_t)es + 4095) / 4096), 256, 0, s, a->dweight, words * (int64_t)es);
+    }
+    return launch_check("loss backward launch");
+  }
+  if (!a->dx && !a->dweight) return FO_OK;
+  const LossBackward b = loss_backward(a, a->dx, a->dweight);
+  FO_TRY(workspace_check(a->workspace, a->workspace_bytes, b.bytes, ar));
+  FO_TRY(ar.disjoint());
+  if (a->dtype == FO_BF16) return run_loss_backward<Bf16>(a, b, s);
+  if (a->dtype == FO_FP16) return run_loss_backward<Fp16>(a, b, s);
+  return run_loss_backward<F32>(a, b, s);
+}
+
+int fo_gated_forward_workspace(const fo_gated* a, int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
+  FO_TRY(gated_checks(a));
+  *bytes = a->rows ? gated_forward(a).bytes : 0;
+  return FO_OK;
+}
+
+int fo_gated_forward(const fo_gated* a, void* stream) {
+  clear_error();
+  FO_TRY(gated_checks(a));
+  Arrays ar;
+  FO_TRY(gated_inputs(a, ar, false));
+  FO_TRY(ar.add(a->y, "y", true, a->rows > 0, a->rows, a->features, a->features, elem_size(a->dtype)));
+  if (a->rows == 0) return FO_OK;
+  const GatedForward f = gated_forward(a);
+  FO_TRY(workspace_check(a->workspace, a->workspace_bytes, f.bytes, ar));
+  FO_TRY(ar.disjoint());
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a->dtype == FO_BF16) return run_gated_forward<Bf16>(a, f, s);
+  if (a->dtype == FO_FP16) return run_gated_forward<Fp16>(a, f, s);
+  return run_gated_forward<F32>(a, f, s);
+}
+
+int fo_gated_backward_workspace(const fo_gated* a, int64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FO_EINVAL, "bytes is NULL");
+  FO_TRY(gated_checks(a));
+  *bytes = a->rows ? gated_backward(a, a->dx, a->dgate || a->dup).bytes : 0;
+  return FO_OK;
+}
+
+int fo_gated_backward(const fo_gated* a, void* stream) {
+  clear_error();
+  FO_TRY(gated_checks(a));
+  const size_t es = elem_size(a->dtype);
+  Arrays ar;
+  FO_TRY(gated_inputs(a, ar, true));
+  FO_TRY(ar.add(a->dy, "dy", false, a->rows > 0, a->rows, a->features, a->dy_ld, es));
+  FO_TRY(ar.add(a->dx, "dx", true, false, a->rows, a->cols, a->cols, es));
+  FO_TRY(ar.add(a->dgate, "dgate", true, false, a->features, a->cols, a->cols, es));
+  FO_TRY(ar.add(a->dup, "dup", true, false, a->features, a->cols, a->cols, es));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a->rows == 0) {
+    FO_TRY(ar.disjoint());
+    const int64_t bytes = a->features * a->cols * (int64_t)es;
+    for (void* out : {a->dgate, a->dup})
+      if (out) hipLaunchKernelGGL(k_zero, grid_of((bytes + 4095) / 4096), 256, 0, s, out, bytes);
+    return launch_check("gated backward launch");
+  }
+  if (!a->dx && !a->dgate && !a->dup) return FO_OK;
+  const GatedBackward b = gated_backward(a, a->dx, a->dgate || a->dup);
+  FO_TRY(workspace_check(a->workspace, a->workspace_bytes, b.bytes, ar));
+  FO_TRY(ar.disjoint());
+  if (a->dtype == FO_BF16) return run_gated_backward<Bf16>(a, b, s);
+  if (a->dtype == FO_FP16) return run_gated_backward<Fp16>(a, b, s);
+  return run_gated_backward<F32>(a, b, s);
+}
+
+}  // extern "C"

@@ -48,7 +48,7 @@ struct F32 {
   typedef v4u_a4 vec;
 };
 template <typename T> constexpr bool is_f32 = false;
-template <> constexpr bool is_f32<F32> = true;
+template <> inline constexpr bool is_f32<F32> = true;
 template <typename T> constexpr int dwords = is_f32<T> ? 8 : 4;     // of one chunk
 
 // One chunk as loaded (still in its type).
