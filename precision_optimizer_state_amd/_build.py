@@ -107,7 +107,19 @@ def build_rows_torch(verbose: bool = False) -> str:
                             [f"-L{OUT_DIR}", "-l:libfoamd.so", "-Wl,-rpath,$ORIGIN", "-lc10_hip"], verbose)
 
 
+STEP_TORCH_SRC = os.path.join(PKG, "csrc", "fo_step_torch.cpp")
+STEP_TORCH_OUT = os.path.join(OUT_DIR, "fo_step_torch.so")
+
+
+def build_step_torch(verbose: bool = False) -> str:
+    """Compile csrc/fo_step_torch.cpp (host C++: clipping, linear cross entropy, the
+    gated block) into lib/fo_step_torch.so, linked to the libfoamd.so beside it."""
+    return _build_extension(STEP_TORCH_SRC, "fo_step_torch", STEP_TORCH_OUT, ["/opt/rocm/include"],
+                            [f"-L{OUT_DIR}", "-l:libfoamd.so", "-Wl,-rpath,$ORIGIN", "-lc10_hip"], verbose)
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
     print(build_marshal(verbose=True))
     print(build_rows_torch(verbose=True))
+    print(build_step_torch(verbose=True))

@@ -39,6 +39,8 @@ import torch
 
 from . import binding as B
 
+STEP_EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "fo_step_torch.so")
+_loaded_step = None
 EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "fo_rows_torch.so")
 _ext = None
 _M64 = (1 << 64) - 1
@@ -59,6 +61,21 @@ def _load():
         ext.set_error(B.FoError)
         _ext = ext
     return _ext
+
+
+def _step_ext():
+    """The host extension of clipping, the loss and the gated block, loaded once."""
+    global _loaded_step
+    if _loaded_step is None:
+        B._load_step()
+        if not os.path.exists(STEP_EXT_PATH):
+            raise ImportError(f"{STEP_EXT_PATH} is missing: build it with __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("fo_step_torch", STEP_EXT_PATH)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.set_error(B.FoError)
+        _loaded_step = ext
+    return _loaded_step
 
 
 def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, state: torch.Tensor | None = None) -> torch.Tensor:
@@ -178,6 +195,40 @@ def dropout_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.
                          state: torch.Tensor | None = None):
     """(h, rms_norm(h)) with h = residual + dropout(x, p)."""
     return _join(x, residual, weight, None, eps, B.FO_RMS_NORM, p, seed, offset, state)
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, *, ignore_index: int = -100,
+                         reduction: str = "mean", label_smoothing: float = 0.0) -> torch.Tensor:
+    """torch.nn.functional.cross_entropy of the logits x weight^T, which are never
+    stored: the last layer of a language model and its loss in one.
+
+    x: (..., cols), weight: (vocab, cols) of the same type, target: int64 of x's
+    leading shape, each in [0, vocab) or ignore_index (the token then has no part in
+    loss or gradients, whatever its x holds).  Any other target makes its token's
+    loss and gradients NaN.  The loss is float32: a scalar ("mean", over the counted
+    tokens, or "sum") or one per token ("none").  The backward pass computes the
+    logits again, a piece of the vocabulary at a time; their gradients are rounded
+    to x's type on the way to those of x and weight."""
+    if reduction not in B.REDUCTION:
+        raise ValueError(f"reduction must be one of {', '.join(B.REDUCTION)}, got {reduction!r}")
+    if not 0.0 <= label_smoothing <= 1.0:
+        raise ValueError(f"label_smoothing must lie in [0, 1], got {label_smoothing}")
+    return (_loaded_step or _step_ext()).linear_cross_entropy(x, weight, target, int(ignore_index),
+                                                              B.REDUCTION[reduction], float(label_smoothing))
+
+
+def gated_linear(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Tensor,
+                 activation: str = "silu") -> torch.Tensor:
+    """act(x gate_weight^T) * (x up_weight^T), the first half of a gated
+    feed-forward block, in one kernel.  x: (..., cols), weights: (features, cols),
+    all of one type; activation: "silu", "gelu" or "gelu_tanh".  For the backward
+    pass the two products are kept in float32 (8 bytes per output element)."""
+    if activation not in B.ACTIVATION:
+        raise ValueError(f"activation must be one of {', '.join(B.ACTIVATION)}, got {activation!r}")
+    return (_loaded_step or _step_ext()).gated_linear(x, gate_weight, up_weight, B.ACTIVATION[activation])
 
 
 # ---------------------------------------------------------------------------

@@ -38,7 +38,7 @@ from typing import Iterable
 
 import torch
 
-from . import binding as B
+from . import binding as B, grads
 
 _W16 = {"bf16": torch.bfloat16, "fp16": torch.float16}
 _ECC = {8: torch.int8, 16: torch.int16}
@@ -242,6 +242,18 @@ class _FlashBase(torch.optim.Optimizer):
                 ps[i].grad = gs[i] = gs[i].to(wdt).contiguous()
             self._step_params(group, ps, gs)
         return loss
+
+    @torch.no_grad()
+    def clip_grad_norm_(self, max_norm, norm_type=2.0, error_if_nonfinite=False):
+        """Scale the gradients of every parameter group in place so that their
+        norm, taken together, is at most max_norm; returns the norm before (see
+        grads.clip_grad_norm_).  Call it between the backward pass and step().
+        With gradient release there is nothing left to clip by then."""
+        if self.grad_release:
+            raise RuntimeError("gradients are stepped and freed during the backward pass (grad_release), before their "
+                               "norm is known")
+        params = [p for group in self.param_groups for p in group["params"]]
+        return grads.clip_grad_norm_(params, max_norm, norm_type, error_if_nonfinite)
 
     def _group(self, p):
         # id -> (group, parameter); the stored parameter guards against a
