@@ -45,7 +45,7 @@ void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStrea
 uint8_t* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : static_cast<uint8_t*>(workspace) + offset; }
 
 void pack(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, hipStream_t s) {
-  const LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)rows, nullptr, 0};
+  const LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, 0, 0, nullptr, 0};
   const unsigned groups = grid_of((rows * dst_ld + 1023) / 1024);
   if (dtype == FO_F32) hipLaunchKernelGGL(k_pack<uint32_t>, groups, 256, 0, s, a);
   else hipLaunchKernelGGL(k_pack<uint16_t>, groups, 256, 0, s, a);
@@ -54,7 +54,9 @@ void pack(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, vo
 // dst: cols rows of dst_ld elements
 void transpose(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, int64_t width,
                const int64_t* target, int64_t ignore, hipStream_t s) {
-  LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)width, target, ignore};
+  const int64_t es = (int64_t)elem_size(dtype);
+  const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (rows == 1 || ld * es % 16 == 0);
+  const LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)width, wide, target, ignore};
   const unsigned groups = grid_of(((width + 63) / 64) * ((cols + 63) / 64));
   if (dtype == FO_F32) hipLaunchKernelGGL(k_transpose<uint32_t>, groups, 256, 0, s, a);
   else hipLaunchKernelGGL(k_transpose<uint16_t>, groups, 256, 0, s, a);
@@ -114,9 +116,11 @@ int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
   float* each = reduced ? (float*)at(a->workspace, f.each) : a->loss;
   const Product p = product_of(w, w_ld, a->vocab, x, x_ld, a->rows, f.k, es);
   launch_product<T, Statistics, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
+  int width = 1;
+  while (width < 16 && width * 256 < a->rows) width *= 2;
   const LossRows r = {part, sums, chosen, a->target, each, a->lse, a->ignore_index, (int)a->rows, 2 * f.c.tiles_r,
-                      (int)a->vocab, (float)a->smoothing};
-  hipLaunchKernelGGL(k_loss_rows, (unsigned)((a->rows + 63) / 64), 1024, 0, s, r);
+                      (int)a->vocab, width, (float)a->smoothing};
+  hipLaunchKernelGGL(k_loss_rows, (unsigned)((a->rows + width - 1) / width), 1024, 0, s, r);
   if (reduced)
     hipLaunchKernelGGL(k_loss_sum, 1, 1024, 0, s, (const float*)each, a->target, a->ignore_index, (int)a->rows,
                        (int)(a->reduction == FO_LOSS_MEAN), a->loss, a->count);

@@ -6,9 +6,10 @@
 // A workgroup of WR x WC waves owns a tile of WR*FR*32 rows of R by WC*FC*32 rows
 // of C and walks along k in steps of 128 bytes (64 elements of a 16-bit type, 32
 // floats).  Rows go from memory straight into LDS, 16 bytes per lane, in a ring of
-// NS stages.  Lane l of a load brings row l / 8 and the 16-byte piece
-// (l % 8) ^ (l / 8 % 8) of it, so that 8 rows read at the same piece lie in 8
-// different 16-byte columns of LDS and no bank is asked twice.
+// NS stages.  Piece c (16 bytes) of row r goes to place c ^ (r / 2 % 8) of the row's
+// 128 bytes: the 16 rows whose piece c is read together then lie in the 16 different
+// 16-byte columns of the 64 banks.  (With r % 8 for r / 2 % 8 rows r and r + 8 share
+// a column, and half of the reads' cycles were bank conflicts.)
 //
 // A wave multiplies FR fragments of 32 rows by FC of 32 rows.  A fragment is 16
 // bytes per lane: row lane % 32, piece 2 s + lane / 32 of sub-step s.  One 16-bit
@@ -113,7 +114,7 @@ struct Tile {
   static constexpr int R = WR * FR * 32, C = WC * FC * 32, waves = WR * WC, threads = waves * 64;
   static constexpr int stage_bytes = (R + C) * kStepBytes, lds_bytes = stage_bytes * NS;
   static constexpr int loads = (R + C) / 8 / waves;            // of a wave, per stage
-  static_assert((R + C) / 8 % waves == 0 && R / 8 % waves == 0, "loads are shared evenly");
+  static_assert((R + C) / 8 % waves == 0 && R / 8 % waves == 0 && waves % 2 == 0, "loads are shared evenly");
 };
 
 // The sums of this wave: acc[i][j] of fragment i of R and j of C.
@@ -131,7 +132,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& at, uint
   constexpr int LR = TL::R / 8 / TL::waves, LC = TL::C / 8 / TL::waves;
   uint32_t off[LR + LC];
   v4u rs[DUAL ? 2 : 1], cs;
-  const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3 & 7)) * 16;
+  const uint32_t piece = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
 #pragma unroll
   for (int i = 0; i < LR; ++i) {
     const int row = (i * TL::waves + wave) * 8 + (lane >> 3);
@@ -181,37 +182,61 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& at, uint
   uint32_t at_r[4], at_c[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const uint32_t x = (uint32_t)(lane & 31) * kStepBytes + (uint32_t)(((2 * s + (lane >> 5)) ^ (lane & 7)) * 16);
+    const uint32_t x = (uint32_t)(lane & 31) * kStepBytes + (uint32_t)(((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
     at_r[s] = x + (uint32_t)(wr * FR * 32) * kStepBytes;
     at_c[s] = x + (uint32_t)(TL::R + wc * FC * 32) * kStepBytes;
   }
 
-#pragma unroll
-  for (int s = 0; s < NS - 1; ++s)
-    if (s < n) fetch(s, s);
-  int stage = 0;
-  for (int k = 0; k < n; ++k) {
-    // stage k has arrived when at most the stages after it are under way
-    if (NS > 2 && k + NS - 2 < n) wait_loads<(NS - 2) * TL::loads>();
-    else wait_loads<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    // every wave has read stage k - 1: its place takes stage k + NS - 1
-    if (k + NS - 1 < n) fetch(k + NS - 1, stage == 0 ? NS - 1 : stage - 1);
+  // Fragments are read one sub-step ahead of the matrix instructions that use them, and
+  // the first of a step before the last instructions of the step before: no wave waits
+  // for LDS with its matrix unit idle.  The scheduling barriers keep that order.
+  v4u fr[2][FR], fc[2][FC];
+  auto read = [&](int s, int stage) {
     const uint8_t* buf = lds_raw + stage * TL::stage_bytes;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4u fr[FR], fc[FC];
+    for (int i = 0; i < FR; ++i) fr[s & 1][i] = *(const v4u*)(buf + at_r[s] + i * 32 * kStepBytes);
 #pragma unroll
-      for (int i = 0; i < FR; ++i) fr[i] = *(const v4u*)(buf + at_r[s] + i * 32 * kStepBytes);
+    for (int j = 0; j < FC; ++j) fc[s & 1][j] = *(const v4u*)(buf + at_c[s] + j * 32 * kStepBytes);
+  };
+  auto use = [&](int s) {
 #pragma unroll
-      for (int j = 0; j < FC; ++j) fc[j] = *(const v4u*)(buf + at_c[s] + j * 32 * kStepBytes);
+    for (int i = 0; i < FR; ++i)
 #pragma unroll
-      for (int i = 0; i < FR; ++i)
+      for (int j = 0; j < FC; ++j) acc[i][j] = mma<T>(fr[s & 1][i], fc[s & 1][j], acc[i][j]);
+  };
+
 #pragma unroll
-        for (int j = 0; j < FC; ++j) acc[i][j] = mma<T>(fr[i], fc[j], acc[i][j]);
+  for (int s = 0; s < NS; ++s)
+    if (s < n) fetch(s, s);
+  if (n >= NS) wait_loads<(NS - 1) * TL::loads>();
+  else wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read(0, 0);
+  int stage = 0;
+  for (int k = 0; k < n; ++k) {
+    const int next = stage == NS - 1 ? 0 : stage + 1;
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      read(s + 1, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      use(s);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    stage = stage == NS - 1 ? 0 : stage + 1;
+    if (k + 1 < n) {
+      // this wave has read all of stage k, and its loads of stage k + 1 have arrived
+      // when at most those of later stages are under way
+      if (NS > 2 && k + NS <= n) wait_loads<(NS - 2) * TL::loads>();
+      else wait_loads<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      // ... and so have the others: stage k's place takes stage k + NS
+      read(0, next);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + NS < n) fetch(k + NS, stage);
+    }
+    use(3);
+    stage = next;
   }
 }
 
