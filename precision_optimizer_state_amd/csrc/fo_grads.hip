@@ -149,8 +149,53 @@ __global__ __launch_bounds__(kBlock) void k_grad_norm_join(const double* sums, i
   if (threadIdx.x == 0) *(FO_GLB float*)norm = (float)v;
 }
 
+// Float32 goes four elements per lane and access, so that a wave's access is one
+// stretch of memory (a chunk of 8 is two accesses 32 bytes apart; QUADS_MEASURED).
+template <typename O>
+__device__ __forceinline__ void clip_tile_f32(const void* grad, void* out, int64_t n, int64_t start, float c) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2), aligned(2)));
+  const float* p = (const float*)grad + start;
+  typename O::raw* o = (typename O::raw*)out + start;
+  const int64_t left = n - start;
+  constexpr int PASSES = kTile / (kBlock * 4);
+  rows::v4u in[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t at = (int64_t)(i * kBlock + threadIdx.x) * 4;
+    if (at + 4 <= left) in[i] = *(const FO_GLB rows::v4u_a4*)(p + at);
+    else
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at + k < left) in[i][k] = __float_as_uint(((const FO_GLB float*)p)[at + k]);
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t at = (int64_t)(i * kBlock + threadIdx.x) * 4;
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(in[i][k]) * c;
+    if (at + 4 <= left) {
+      if constexpr (rows::is_f32<O>) {
+        const rows::v4u w = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+        *(FO_GLB rows::v4u_a4*)(o + at) = w;
+      } else {
+        const v2u w = {O::pack(f[0], f[1]), O::pack(f[2], f[3])};
+        __builtin_nontemporal_store(w, (FO_GLB v2u*)(o + at));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at + k < left) {
+          if constexpr (rows::is_f32<O>) ((FO_GLB float*)o)[at + k] = f[k];
+          else ((FO_GLB uint16_t*)o)[at + k] = (uint16_t)O::pack(f[k], f[k]);
+        }
+    }
+  }
+}
+
 template <typename T, typename O>
 __device__ __forceinline__ void clip_tile(const void* grad, void* out, int64_t n, int64_t start, float c) {
+  if constexpr (rows::is_f32<T>) return clip_tile_f32<O>(grad, out, n, start, c);
   const typename T::raw* p = (const typename T::raw*)grad + start;
   typename O::raw* o = (typename O::raw*)out + start;
   const int64_t left = n - start;

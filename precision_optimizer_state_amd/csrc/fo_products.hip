@@ -37,9 +37,10 @@ template <typename T, typename E, bool NARROW_OK>
 void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStream_t s) {
   p.tiles_r = c.tiles_r; p.tiles_c = c.tiles_c; p.slices = c.slices;
   if constexpr (NARROW_OK)
-    if (c.kind == NARROW) return launch_tile<T, E, 2, 1, 2, 1, 4>(p, e, s);
+    if (c.kind == NARROW) return launch_tile<T, E, 1, 1, 2, 1, 4>(p, e, s);
   if (c.kind == WIDE) return launch_tile<T, E, 2, 4, 4, 2, 2>(p, e, s);
-  launch_tile<T, E, 2, 2, 2, 2, 2>(p, e, s);
+  if (c.kind == MIDDLE) return launch_tile<T, E, 2, 2, 2, 2, 2>(p, e, s);
+  launch_tile<T, E, 1, 2, 2, 1, 4>(p, e, s);
 }
 
 uint8_t* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : static_cast<uint8_t*>(workspace) + offset; }
@@ -118,7 +119,7 @@ int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
   launch_product<T, Statistics, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
   int width = 1;
   while (width < 16 && width * 256 < a->rows) width *= 2;
-  const LossRows r = {part, sums, chosen, a->target, each, a->lse, a->ignore_index, (int)a->rows, 2 * f.c.tiles_r,
+  const LossRows r = {part, sums, chosen, a->target, each, a->lse, a->ignore_index, (int)a->rows, waves_r(f.c.kind) * f.c.tiles_r,
                       (int)a->vocab, width, (float)a->smoothing};
   hipLaunchKernelGGL(k_loss_rows, (unsigned)((a->rows + width - 1) / width), 1024, 0, s, r);
   if (reduced)

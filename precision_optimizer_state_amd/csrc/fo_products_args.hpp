@@ -45,10 +45,12 @@ struct Layout {
 };
 
 // Tile kinds of k_product (R x C).
-enum TileKind { WIDE, MIDDLE, NARROW };
+enum TileKind { WIDE, MIDDLE, SMALL, NARROW };
 struct Cut { TileKind kind; int tiles_r, tiles_c, slices; };
-constexpr int tile_r(TileKind k) { return k == WIDE ? 256 : 128; }
-constexpr int tile_c(TileKind k) { return k == WIDE ? 256 : k == MIDDLE ? 128 : 32; }
+constexpr int tile_r(TileKind k) { return k == WIDE ? 256 : k == MIDDLE ? 128 : 64; }
+constexpr int tile_c(TileKind k) { return k == WIDE ? 256 : k == MIDDLE ? 128 : k == SMALL ? 64 : 32; }
+// waves that share a tile's rows of R: each has a part of them to itself
+constexpr int waves_r(TileKind k) { return k == WIDE || k == MIDDLE ? 2 : 1; }
 constexpr int64_t kUnits = 256;                                 // compute units
 
 // nr (with `dual`, of each of two matrices) rows of R against nc of C, `steps` of k.
@@ -63,7 +65,7 @@ inline Cut cut(int64_t nr, int64_t nc, int64_t steps, bool dual, bool narrow_ok,
   };
   int64_t n;
   if (narrow_ok && nc <= 32) n = tiles(NARROW);
-  else if ((n = tiles(WIDE)) < kUnits) n = tiles(MIDDLE);
+  else if ((n = tiles(WIDE)) < kUnits && (n = tiles(MIDDLE)) < kUnits) n = tiles(SMALL);
   c.slices = 1;
   if (sliced) c.slices = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kUnits / n, steps / 8, 32}));
   return c;
@@ -92,7 +94,7 @@ inline LossForward loss_forward(const fo_loss* a) {
   if (!direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) f.x = l.take(a->rows * f.k * es);
   if (!direct(a->weight, a->vocab, a->cols, a->weight_ld, a->dtype)) f.w = l.take(a->vocab * f.k * es);
   f.c = cut(a->vocab, a->rows, f.k * es / 128, false, true, false);
-  const int64_t parts = 2 * (int64_t)f.c.tiles_r;               // two waves share a tile's rows of R
+  const int64_t parts = (int64_t)waves_r(f.c.kind) * f.c.tiles_r;
   f.part = l.take(parts * a->rows * 8);
   if (a->smoothing != 0.0) f.sums = l.take(parts * a->rows * 4);
   f.chosen = l.take(a->rows * 4);

@@ -114,7 +114,7 @@ struct Tile {
   static constexpr int R = WR * FR * 32, C = WC * FC * 32, waves = WR * WC, threads = waves * 64;
   static constexpr int stage_bytes = (R + C) * kStepBytes, lds_bytes = stage_bytes * NS;
   static constexpr int loads = (R + C) / 8 / waves;            // of a wave, per stage
-  static_assert((R + C) / 8 % waves == 0 && R / 8 % waves == 0 && waves % 2 == 0, "loads are shared evenly");
+  static_assert((R + C) / 8 % waves == 0 && R / 8 % waves == 0, "loads are shared evenly");
 };
 
 // The sums of this wave: acc[i][j] of fragment i of R and j of C.
@@ -132,17 +132,18 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& at, uint
   constexpr int LR = TL::R / 8 / TL::waves, LC = TL::C / 8 / TL::waves;
   uint32_t off[LR + LC];
   v4u rs[DUAL ? 2 : 1], cs;
-  const uint32_t piece = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
+  // (a load's rows begin at a multiple of 8, so r / 2 % 8 is 4 on its odd chunks and lane / 16)
+  auto piece = [&](int i) { return (uint32_t)((lane & 7) ^ (((i * TL::waves + wave) & 1) * 4 + (lane >> 4))) * 16; };
 #pragma unroll
   for (int i = 0; i < LR; ++i) {
     const int row = (i * TL::waves + wave) * 8 + (lane >> 3);
     const int src = DUAL ? row / 64 * 32 + row % 32 : row;
-    off[i] = (uint32_t)min(src, p.nr - 1 - r0) * (uint32_t)p.r_ld + piece;
+    off[i] = (uint32_t)min(src, p.nr - 1 - r0) * (uint32_t)p.r_ld + piece(i);
   }
 #pragma unroll
   for (int i = 0; i < LC; ++i) {
     const int row = (i * TL::waves + wave) * 8 + (lane >> 3);
-    off[LR + i] = (uint32_t)min(row, p.nc - 1 - c0) * (uint32_t)p.c_ld + piece;
+    off[LR + i] = (uint32_t)min(row, p.nc - 1 - c0) * (uint32_t)p.c_ld + piece(i);
   }
   const uint32_t k_bytes = (uint32_t)p.steps * kStepBytes;
   const uint32_t r_rows = (uint32_t)min(DUAL ? TL::R / 2 : TL::R, p.nr - r0), c_rows = (uint32_t)min(TL::C, p.nc - c0);
