@@ -27,48 +27,51 @@ int launch_check(const char* what) {
 
 unsigned grid_of(int64_t want, int64_t most = 1 << 16) { return (unsigned)std::max<int64_t>(1, std::min(want, most)); }
 
-template <typename T, typename E, int WR, int WC, int FR, int FC, int NS>
+template <typename T, typename E, Form F, int WR, int WC, int FR, int FC, int NS>
 void launch_tile(const Product& p, const typename E::Args& e, hipStream_t s) {
   const unsigned groups = (unsigned)p.tiles_r * (unsigned)p.tiles_c * (unsigned)p.slices;
-  hipLaunchKernelGGL((k_product<T, WR, WC, FR, FC, NS, E>), groups, WR * WC * 64, 0, s, p, e);
+  hipLaunchKernelGGL((k_product<T, WR, WC, FR, FC, NS, F, E>), groups, WR * WC * 64, 0, s, p, e);
 }
 
-template <typename T, typename E, bool NARROW_OK>
+template <typename T, typename E, Form F, bool NARROW_OK>
 void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStream_t s) {
   p.tiles_r = c.tiles_r; p.tiles_c = c.tiles_c; p.slices = c.slices;
   if constexpr (NARROW_OK)
-    if (c.kind == NARROW) return launch_tile<T, E, 1, 1, 2, 1, 4>(p, e, s);
-  if (c.kind == WIDE) return launch_tile<T, E, 2, 4, 4, 2, 2>(p, e, s);
-  if (c.kind == MIDDLE) return launch_tile<T, E, 2, 2, 2, 2, 2>(p, e, s);
-  launch_tile<T, E, 1, 2, 2, 1, 4>(p, e, s);
+    if (c.kind == NARROW) return launch_tile<T, E, F, 1, 1, 2, 1, 4>(p, e, s);
+  if (c.kind == WIDE) return launch_tile<T, E, F, 2, 4, 4, 2, 2>(p, e, s);
+  if (c.kind == MIDDLE) return launch_tile<T, E, F, 2, 2, 2, 2, 2>(p, e, s);
+  launch_tile<T, E, F, 1, 2, 2, 1, 4>(p, e, s);
 }
 
 uint8_t* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : static_cast<uint8_t*>(workspace) + offset; }
 
-void pack(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, hipStream_t s) {
-  const LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, 0, 0, nullptr, 0};
-  const unsigned groups = grid_of((rows * dst_ld + 1023) / 1024);
+// dst: dst_rows rows of dst_ld elements
+void pack(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, int64_t dst_rows,
+          const int64_t* target, int64_t ignore, hipStream_t s) {
+  const int64_t es = (int64_t)elem_size(dtype);
+  const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (rows == 1 || ld * es % 16 == 0);
+  const PackArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)dst_rows, wide, target, ignore};
+  const unsigned groups = grid_of((dst_rows * dst_ld * es / 16 + 511) / 512);
   if (dtype == FO_F32) hipLaunchKernelGGL(k_pack<uint32_t>, groups, 256, 0, s, a);
   else hipLaunchKernelGGL(k_pack<uint16_t>, groups, 256, 0, s, a);
 }
 
-// dst: cols rows of dst_ld elements
-void transpose(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, int64_t width,
-               const int64_t* target, int64_t ignore, hipStream_t s) {
-  const int64_t es = (int64_t)elem_size(dtype);
-  const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (rows == 1 || ld * es % 16 == 0);
-  const LayoutArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)width, wide, target, ignore};
-  const unsigned groups = grid_of(((width + 63) / 64) * ((cols + 63) / 64));
-  if (dtype == FO_F32) hipLaunchKernelGGL(k_transpose<uint32_t>, groups, 256, 0, s, a);
-  else hipLaunchKernelGGL(k_transpose<uint16_t>, groups, 256, 0, s, a);
+// An operand as its product reads it: the caller's rows, or a copy in the workspace.
+struct Operand { const void* p; int64_t ld; };
+Operand operand(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* workspace, int64_t offset, int64_t k,
+                hipStream_t s) {
+  if (offset < 0) return {src, ld};
+  pack(dtype, src, ld, rows, cols, at(workspace, offset), k, rows, nullptr, 0, s);
+  return {at(workspace, offset), k};
 }
 
-Product product_of(const void* r, int64_t r_ld, int64_t nr, const void* c, int64_t c_ld, int64_t nc, int64_t k, int64_t es) {
+Product product_of(const Operand& r, int64_t nr, const Operand& c, int64_t nc, int64_t k, int64_t es) {
   Product p = {};
-  p.r = r; p.c = c;
-  p.r_ld = r_ld * es; p.c_ld = c_ld * es;
+  p.r = r.p; p.c = c.p;
+  p.r_ld = r.ld * es; p.c_ld = c.ld * es;
   p.nr = (int)nr; p.nc = (int)nc;
-  p.steps = (int)(k * es / 128);
+  p.k = (int)k;
+  p.steps = (int)((k * es + 127) / 128);
   return p;
 }
 
@@ -106,17 +109,15 @@ int workspace_check(void* workspace, int64_t have, int64_t need, Arrays& ar) {
 template <typename T>
 int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
-  const void *x = a->x, *w = a->weight;
-  int64_t x_ld = a->x_ld, w_ld = a->weight_ld;
-  if (f.x >= 0) { pack(a->dtype, x, x_ld, a->rows, a->cols, at(a->workspace, f.x), f.k, s); x = at(a->workspace, f.x); x_ld = f.k; }
-  if (f.w >= 0) { pack(a->dtype, w, w_ld, a->vocab, a->cols, at(a->workspace, f.w), f.k, s); w = at(a->workspace, f.w); w_ld = f.k; }
+  const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, a->workspace, f.x, f.k, s);
+  const Operand w = operand(a->dtype, a->weight, a->weight_ld, a->vocab, a->cols, a->workspace, f.w, f.k, s);
   const bool reduced = a->reduction != FO_LOSS_NONE;
   v2f* part = (v2f*)at(a->workspace, f.part);
   float* sums = (float*)at(a->workspace, f.sums);
   float* chosen = (float*)at(a->workspace, f.chosen);
   float* each = reduced ? (float*)at(a->workspace, f.each) : a->loss;
-  const Product p = product_of(w, w_ld, a->vocab, x, x_ld, a->rows, f.k, es);
-  launch_product<T, Statistics, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
+  const Product p = product_of(w, a->vocab, x, a->rows, f.k, es);
+  launch_product<T, Statistics, ROWS_ROWS, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
   int width = 1;
   while (width < 16 && width * 256 < a->rows) width *= 2;
   const LossRows r = {part, sums, chosen, a->target, each, a->lse, a->ignore_index, (int)a->rows, waves_r(f.c.kind) * f.c.tiles_r,
@@ -132,48 +133,45 @@ template <typename T>
 int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
   void* ws = a->workspace;
-  float *f = (float*)at(ws, b.f), *unit = (float*)at(ws, b.unit), *factor = (float*)at(ws, b.factor);
+  float *unit = (float*)at(ws, b.unit), *factor = (float*)at(ws, b.factor);
   const bool none = a->reduction == FO_LOSS_NONE;
   hipLaunchKernelGGL(k_loss_factors, 1, 1024, 0, s, a->dloss, none ? a->dloss_ld : (int64_t)0,
                      a->reduction == FO_LOSS_MEAN ? (const float*)a->count : (const float*)nullptr, a->target, a->ignore_index,
-                     (int)a->rows, f, unit, factor);
-  const void* x = a->x;
-  int64_t x_ld = a->x_ld;
-  if (b.x >= 0) { pack(a->dtype, x, x_ld, a->rows, a->cols, at(ws, b.x), b.k, s); x = at(ws, b.x); x_ld = b.k; }
-  if (a->dweight) transpose(a->dtype, a->x, a->x_ld, a->rows, a->cols, at(ws, b.xt), b.n, b.n, a->target, a->ignore_index, s);
+                     (int)a->rows, unit, factor);
+  const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, ws, b.x, b.k, s);
+  // dweight reads x without the tokens that are not counted: 0 times what they hold need not be 0
+  if (a->dweight)
+    pack(a->dtype, a->x, a->x_ld, a->rows, a->cols, at(ws, b.xm), b.k, b.n, a->target, a->ignore_index, s);
   // half precision holds gradients of logits times 2^15
   const float scale = __is_same(T, Fp16) ? 32768.0f : 1.0f;
   const int64_t slice = a->rows * b.sums_ld;
   for (int64_t first = 0; first < a->vocab; first += b.piece) {
     const int64_t nv = std::min(b.piece, a->vocab - first), nvp = padded(nv);
-    const uint8_t* w_at = static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es;
-    const void* w = w_at;
-    int64_t w_ld = a->weight_ld;
-    if (b.w >= 0) { pack(a->dtype, w, w_ld, nv, a->cols, at(ws, b.w), b.k, s); w = at(ws, b.w); w_ld = b.k; }
-    const Product pz = product_of(w, w_ld, nv, x, x_ld, a->rows, b.k, es);
+    const Operand w = operand(a->dtype, static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es, a->weight_ld, nv,
+                              a->cols, ws, b.w, b.k, s);
+    const Operand dz = {at(ws, b.dz), nvp};
+    const Product pz = product_of(w, nv, x, a->rows, b.k, es);
     // tokens in whole steps: the padding is written too (as zeros)
-    const Cut cz = cut(nv, b.n, pz.steps, false, false, false);
-    launch_product<T, LogitGradients, false>(
-        pz, cz, {at(ws, b.by_token), at(ws, b.by_place), nvp, b.n, a->lse, unit, a->target, a->ignore_index, (int)first,
-                 (int)a->vocab, scale, (float)a->smoothing}, s);
+    launch_product<T, LogitGradients, ROWS_ROWS, false>(
+        pz, cut(nv, b.n, pz.steps, false, false, false),
+        {at(ws, b.dz), nvp, a->lse, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
+         (float)a->smoothing}, s);
     if (a->dx) {
-      transpose(a->dtype, w_at, a->weight_ld, nv, a->cols, at(ws, b.wt), nvp, nvp, nullptr, 0, s);
-      const Product px = product_of(at(ws, b.wt), nvp, a->cols, at(ws, b.by_token), nvp, a->rows, nvp, es);
-      Cut cx = cut(a->cols, a->rows, px.steps, false, true, false);
-      cx.slices = b.slices;
-      launch_product<T, KeepSums, true>(px, cx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
+      Product px = product_of(w, a->cols, dz, a->rows, nvp, es);
+      px.k = (int)nv;
+      launch_product<T, KeepSums, COLS_ROWS, true>(px, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
     }
     if (a->dweight) {
-      const Product pw = product_of(at(ws, b.xt), b.n, a->cols, at(ws, b.by_place), b.n, nv, b.n, es);
-      const Cut cw = cut(a->cols, nv, pw.steps, false, true, false);
-      launch_product<T, StoreScaled, true>(
-          pw, cw, {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
-                   1.0f / scale}, s);
+      const Product pw = product_of({at(ws, b.xm), b.k}, a->cols, dz, nv, b.n, es);
+      launch_product<T, StoreScaled, COLS_COLS, true>(
+          pw, cut(a->cols, nv, pw.steps, false, true, false),
+          {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
+           1.0f / scale}, s);
     }
   }
   if (a->dx) {
-    const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.slices, a->dx, f, a->target, a->ignore_index,
-                        (int)a->rows, (int)a->cols, 1.0f / scale};
+    const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.dx.slices, a->dx, factor, a->target,
+                        a->ignore_index, (int)a->rows, (int)a->cols, 1.0f / scale};
     hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
   }
   return launch_check("loss backward launch");
@@ -208,18 +206,12 @@ int gated_inputs(const fo_gated* a, Arrays& ar, bool backward) {
 template <typename T>
 int run_gated_forward(const fo_gated* a, const GatedForward& f, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
-  void* ws = a->workspace;
-  const void *x = a->x, *gate = a->gate, *up_w = a->up;
-  int64_t x_ld = a->x_ld, w_ld = a->gate_ld;
-  if (f.x >= 0) { pack(a->dtype, x, x_ld, a->rows, a->cols, at(ws, f.x), f.k, s); x = at(ws, f.x); x_ld = f.k; }
-  if (f.gate >= 0) {
-    pack(a->dtype, gate, a->gate_ld, a->features, a->cols, at(ws, f.gate), f.k, s);
-    pack(a->dtype, up_w, a->up_ld, a->features, a->cols, at(ws, f.up), f.k, s);
-    gate = at(ws, f.gate); up_w = at(ws, f.up); w_ld = f.k;
-  }
-  Product p = product_of(gate, w_ld, a->features, x, x_ld, a->rows, f.k, es);
-  p.r2 = up_w;
-  launch_product<T, Gated, true>(p, f.c, {a->y, a->g, a->u, a->activation}, s);
+  const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, a->workspace, f.x, f.k, s);
+  const Operand gate = operand(a->dtype, a->gate, a->gate_ld, a->features, a->cols, a->workspace, f.gate, f.k, s);
+  const Operand up_w = operand(a->dtype, a->up, a->up_ld, a->features, a->cols, a->workspace, f.up, f.k, s);
+  Product p = product_of(gate, a->features, x, a->rows, f.k, es);
+  p.r2 = up_w.p;
+  launch_product<T, Gated, DUAL_ROWS, true>(p, f.c, {a->y, a->g, a->u, a->activation}, s);
   return launch_check("gated forward launch");
 }
 
@@ -227,30 +219,34 @@ template <typename T>
 int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s) {
   const int64_t es = elem_bytes<T>, half = b.half;
   void* ws = a->workspace;
-  const GatedBwd g = {a->dy, a->dy_ld, a->g, a->u, at(ws, b.by_token), 2 * half, at(ws, b.by_feature), b.n,
-                      (int)a->rows, (int)a->features, (int)half, a->activation};
-  hipLaunchKernelGGL((k_gated_bwd<T>), grid_of((b.n / 64) * (half / 64)), 256, 0, s, g);
+  const GatedBwd g = {a->dy, a->dy_ld, a->g, a->u, at(ws, b.d), (int)a->rows, (int)b.n, (int)a->features, (int)half,
+                      a->activation};
+  hipLaunchKernelGGL((k_gated_bwd<T>), grid_of((b.n * half / 8 + 255) / 256), 256, 0, s, g);
+  const Operand d = {at(ws, b.d), 2 * half};
   if (a->dx) {
-    uint8_t* wt = at(ws, b.wt);
-    transpose(a->dtype, a->gate, a->gate_ld, a->features, a->cols, wt, 2 * half, half, nullptr, 0, s);
-    transpose(a->dtype, a->up, a->up_ld, a->features, a->cols, wt + half * es, 2 * half, half, nullptr, 0, s);
-    const Product p = product_of(wt, 2 * half, a->cols, at(ws, b.by_token), 2 * half, a->rows, 2 * half, es);
-    if (b.c_dx.slices > 1) {
+    const Operand gate = operand(a->dtype, a->gate, a->gate_ld, a->features, a->cols, ws, b.gate, b.k, s);
+    const Operand up_w = operand(a->dtype, a->up, a->up_ld, a->features, a->cols, ws, b.up, b.k, s);
+    Product p = product_of(gate, a->cols, d, a->rows, 2 * half, es);
+    p.r2 = up_w.p;
+    p.k = (int)a->features;
+    p.joint = (int)(half * es / 128);
+    if (b.dx.slices > 1) {
       const int64_t slice = a->rows * b.sums_ld;
-      launch_product<T, KeepSums, true>(p, b.c_dx, {(float*)at(ws, b.sums), b.sums_ld, slice, 0}, s);
-      const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.c_dx.slices, a->dx, nullptr, nullptr, 0,
+      launch_product<T, KeepSums, COLS_ROWS, true>(p, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, 0}, s);
+      const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.dx.slices, a->dx, nullptr, nullptr, 0,
                           (int)a->rows, (int)a->cols, 1.0f};
       hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
     } else {
-      launch_product<T, StoreScaled, true>(p, b.c_dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, nullptr, 1.0f}, s);
+      launch_product<T, StoreScaled, COLS_ROWS, true>(p, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, nullptr, 1.0f}, s);
     }
   }
   if (a->dgate || a->dup) {
-    transpose(a->dtype, a->x, a->x_ld, a->rows, a->cols, at(ws, b.xt), b.n, b.n, nullptr, 0, s);
-    const Product p = product_of(at(ws, b.xt), b.n, a->cols, at(ws, b.by_feature), b.n, 2 * half, b.n, es);
-    const Cut c = cut(a->cols, 2 * half, p.steps, false, true, false);
-    launch_product<T, StoreScaled, true>(
-        p, c, {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, nullptr, 1.0f}, s);
+    const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, ws, b.x, b.k, s);
+    Product p = product_of(x, a->cols, d, 2 * half, b.n, es);
+    p.k = (int)a->rows;
+    launch_product<T, StoreScaled, COLS_COLS, true>(
+        p, cut(a->cols, 2 * half, p.steps, false, true, false),
+        {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, nullptr, 1.0f}, s);
   }
   return launch_check("gated backward launch");
 }

@@ -71,9 +71,9 @@ inline Cut cut(int64_t nr, int64_t nc, int64_t steps, bool dual, bool narrow_ok,
   return c;
 }
 
-// Vocabulary per piece of the backward pass: the logits' gradients of a piece, both
-// ways round, are at most about 2^27 elements each (512 MB in 16 bits).
-constexpr int64_t kPieceElems = int64_t(1) << 27;
+// Vocabulary per piece of the backward pass: the logits' gradients of a piece are at
+// most about 2^28 elements (512 MB in 16 bits).
+constexpr int64_t kPieceElems = int64_t(1) << 28;
 inline int64_t piece_vocab(int64_t tokens, int64_t vocab) {
   const int64_t most = std::max<int64_t>(1024, kPieceElems / padded(tokens));
   const int64_t pieces = (vocab + most - 1) / most;
@@ -104,9 +104,9 @@ inline LossForward loss_forward(const fo_loss* a) {
 }
 
 struct LossBackward {
-  int64_t f, unit, factor, x = -1, w = -1, xt = -1, wt = -1, by_token = -1, by_place = -1, sums = -1, bytes = 0;
+  int64_t unit, factor, x = -1, w = -1, xm = -1, dz = -1, sums = -1, bytes = 0;
   int64_t k, n, piece, sums_ld;                                 // columns and tokens in whole steps; vocabulary per piece
-  int slices = 1;
+  Cut dx = {};                                                  // of a whole piece
 };
 inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   LossBackward b;
@@ -115,21 +115,16 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   b.k = a->cols % (128 / es) ? padded(a->cols) : a->cols;
   b.n = padded(a->rows);
   b.piece = piece_vocab(a->rows, a->vocab);
-  b.f = l.take(a->rows * 4);
   b.unit = l.take(a->rows * 4);
   b.factor = l.take(4);
   if (!direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) b.x = l.take(a->rows * b.k * es);
   if (!direct(a->weight, a->vocab, a->cols, a->weight_ld, a->dtype)) b.w = l.take(std::min(b.piece, a->vocab) * b.k * es);
-  if (dw) {
-    b.xt = l.take(a->cols * b.n * es);
-    b.by_place = l.take(b.piece * b.n * es);
-  }
+  if (dw) b.xm = l.take(b.n * b.k * es);
+  b.dz = l.take(b.n * b.piece * es);
   b.sums_ld = up(a->cols, 4);
   if (dx) {
-    b.wt = l.take(a->cols * b.piece * es);
-    b.by_token = l.take(a->rows * b.piece * es);
-    b.slices = cut(a->cols, a->rows, b.piece * es / 128, false, true, true).slices;
-    b.sums = l.take((int64_t)b.slices * a->rows * b.sums_ld * 4);
+    b.dx = cut(a->cols, a->rows, b.piece * es / 128, false, true, true);
+    b.sums = l.take((int64_t)b.dx.slices * a->rows * b.sums_ld * 4);
   }
   b.bytes = l.bytes;
   return b;
@@ -154,27 +149,29 @@ inline GatedForward gated_forward(const fo_gated* a) {
 }
 
 struct GatedBackward {
-  int64_t by_token = -1, by_feature = -1, wt = -1, xt = -1, sums = -1, bytes = 0;
-  int64_t half, n, sums_ld;
-  Cut c_dx = {};
+  int64_t d = -1, x = -1, gate = -1, up = -1, sums = -1, bytes = 0;
+  int64_t k, half, n, sums_ld;
+  Cut dx = {};
 };
 inline GatedBackward gated_backward(const fo_gated* a, bool dx, bool dw) {
   GatedBackward b;
   Layout l;
   const int64_t es = (int64_t)elem_size(a->dtype);
+  b.k = a->cols % (128 / es) ? padded(a->cols) : a->cols;
   b.half = padded(a->features);
   b.n = padded(a->rows);
   b.sums_ld = up(a->cols, 4);
+  b.d = l.take(b.n * 2 * b.half * es);
   if (dx) {
-    b.by_token = l.take(a->rows * 2 * b.half * es);
-    b.wt = l.take(a->cols * 2 * b.half * es);
-    b.c_dx = cut(a->cols, a->rows, 2 * b.half * es / 128, false, true, true);
-    if (b.c_dx.slices > 1) b.sums = l.take((int64_t)b.c_dx.slices * a->rows * b.sums_ld * 4);
+    if (!direct(a->gate, a->features, a->cols, a->gate_ld, a->dtype) ||
+        !direct(a->up, a->features, a->cols, a->up_ld, a->dtype) || a->gate_ld != a->up_ld) {
+      b.gate = l.take(a->features * b.k * es);
+      b.up = l.take(a->features * b.k * es);
+    }
+    b.dx = cut(a->cols, a->rows, 2 * b.half * es / 128, false, true, true);
+    if (b.dx.slices > 1) b.sums = l.take((int64_t)b.dx.slices * a->rows * b.sums_ld * 4);
   }
-  if (dw) {
-    b.by_feature = l.take(2 * b.half * b.n * es);
-    b.xt = l.take(a->cols * b.n * es);
-  }
+  if (dw && !direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) b.x = l.take(a->rows * b.k * es);
   b.bytes = l.bytes;
   return b;
 }

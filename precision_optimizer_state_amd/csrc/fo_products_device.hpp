@@ -1,23 +1,30 @@
 // fo_products_device.hpp -- the matrix product that the products' kernels share:
 //   out[c][r] = sum over k of C[c][k] * R[r][k]
-// for two operands whose rows are contiguous along k, on the matrix cores.
-// What becomes of a tile of sums is the epilogue's (fo_products_kernels.hpp).
+// on the matrix cores.  Either operand may lie in memory by rows (rows r, k contiguous)
+// or by columns (rows k, r contiguous).  What becomes of a tile of sums is the
+// epilogue's (fo_products_kernels.hpp).
 //
-// A workgroup of WR x WC waves owns a tile of WR*FR*32 rows of R by WC*FC*32 rows
-// of C and walks along k in steps of 128 bytes (64 elements of a 16-bit type, 32
-// floats).  Rows go from memory straight into LDS, 16 bytes per lane, in a ring of
-// NS stages.  Piece c (16 bytes) of row r goes to place c ^ (r / 2 % 8) of the row's
-// 128 bytes: the 16 rows whose piece c is read together then lie in the 16 different
-// 16-byte columns of the 64 banks.  (With r % 8 for r / 2 % 8 rows r and r + 8 share
-// a column, and half of the reads' cycles were bank conflicts.)
+// A workgroup of WR x WC waves owns a tile of WR*FR*32 rows of R by WC*FC*32 rows of C
+// and walks along k in steps of 128 bytes (64 elements of a 16-bit type, 32 floats).
+// Operands go from memory straight into LDS, 16 bytes ("a piece") per lane, in a ring
+// of NS stages.
 //
-// A wave multiplies FR fragments of 32 rows by FC of 32 rows.  A fragment is 16
-// bytes per lane: row lane % 32, piece 2 s + lane / 32 of sub-step s.  One 16-bit
-// matrix instruction takes a whole fragment (32x32x16); four float ones (32x32x2)
-// take a float each: the order along k is permuted, the same way on both sides.
-// Sums are float32.  Lane l holds 16 sums of column c = l % 32 of the fragment
+// A wave multiplies FR fragments of 32 rows by FC of 32 rows.  A fragment is 16 bytes
+// per lane: row lane % 32, elements of k from piece 2 s + lane / 32 of sub-step s.  One
+// 16-bit matrix instruction takes a whole fragment (32x32x16); four float ones
+// (32x32x2) take a float each: the order along k is permuted, the same way on both
+// sides.  Sums are float32.  Lane l holds 16 sums of column c = l % 32 of the fragment
 // pair, of rows r = 8 (i / 4) + 4 (l / 32) + i % 4: four neighbours in r at a time,
 // which is the direction in which outputs are contiguous.
+//
+// LDS by rows: piece p of row r at place p ^ (r / 2 % 8) of the row's 128 bytes; the 16
+// rows whose piece p is read together lie in the 16 different 16-byte columns of the 64
+// banks.  (With r % 8 for r / 2 % 8 rows r and r + 8 share a column, and half of the
+// reads' cycles were bank conflicts.)
+// LDS by columns: a row of k holds the tile's pieces, permuted in fours by k so that
+// the four rows of k that a transposing read touches (16-bit types: ds_read_b64_tr_b16,
+// 16 lanes reading 4 rows of 16 elements get a column of 4 each) lie in different
+// banks.  Floats are read one by one.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -59,15 +66,27 @@ __device__ __forceinline__ v16f mma(v4u r, v4u c, v16f acc) {
   }
 }
 
-// One product: R is nr x k, C is nc x k, rows `ld` bytes apart, k a multiple of a
-// step (operands are padded with zeros), everything 16-byte aligned.  With two
-// matrices in R (`r2`) fragments of 32 rows alternate between them.
+// How a product's operands lie.
+enum Form {
+  ROWS_ROWS,      // both by rows
+  DUAL_ROWS,      // both by rows; fragments of 32 rows of R alternate between r and r2
+  COLS_ROWS,      // R by columns; with r2, steps of k from `joint` on are r2's
+  COLS_COLS,      // both by columns
+};
+
+// One product: R is nr x k, C is nc x k.  `ld`: bytes from one row (of memory) to the
+// next.  Everything is 16-byte aligned.  By rows k is a multiple of a step (padded with
+// zeros).  By columns rows of memory are whole pieces long; C has a row for every k of
+// its steps, of R there may be fewer (`k`, of each of r and r2): the last is read again
+// for those, which C has as 0.
 struct Product {
   const void* r;
   const void* r2;
   const void* c;
-  int64_t r_ld, c_ld;       // bytes
+  int64_t r_ld, c_ld;
   int nr, nc;               // rows
+  int k;                    // R by columns: rows of k
+  int joint;                // COLS_ROWS: steps of r
   int steps;                // of k
   int tiles_r, tiles_c;
   int slices;               // of k: slice s takes steps [s * steps / slices, (s + 1) * steps / slices)
@@ -117,76 +136,147 @@ struct Tile {
   static_assert((R + C) / 8 % waves == 0 && R / 8 % waves == 0, "loads are shared evenly");
 };
 
-// The sums of this wave: acc[i][j] of fragment i of R and j of C.
-template <typename T, typename TL, int WR, int WC, int FR, int FC, int NS, bool DUAL>
-__device__ __forceinline__ void multiply(const Product& p, const Place& at, uint8_t* lds_raw, v16f (&acc)[FR][FC]) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds_raw;
-  const int r0 = at.r * (DUAL ? TL::R / 2 : TL::R), c0 = at.c * TL::C;
-  const int first = (int)((int64_t)at.slice * p.steps / p.slices);
-  const int n = (int)((int64_t)(at.slice + 1) * p.steps / p.slices) - first;
+// One operand's loads and reads.  N: rows of the tile; F: fragments of a wave.
+// By rows.  DUAL: fragments of 32 rows alternate between two matrices.
+template <typename T, int N, int F, int WAVES, bool DUAL>
+struct ByRows {
+  static constexpr int loads = N / 8 / WAVES;
+  uint32_t off[loads], at[4];
+  v4u buf[DUAL ? 2 : 1];
 
-  // offsets of this lane's loads from the tile's first row; rows past the last are
-  // read as the last one again (their sums are not used)
-  constexpr int LR = TL::R / 8 / TL::waves, LC = TL::C / 8 / TL::waves;
-  uint32_t off[LR + LC];
-  v4u rs[DUAL ? 2 : 1], cs;
-  // (a load's rows begin at a multiple of 8, so r / 2 % 8 is 4 on its odd chunks and lane / 16)
-  auto piece = [&](int i) { return (uint32_t)((lane & 7) ^ (((i * TL::waves + wave) & 1) * 4 + (lane >> 4))) * 16; };
+  // rows past the last are read as the last again (their sums are not used)
+  __device__ __forceinline__ void init(const void* base, const void* base2, int64_t ld, int row0, int rows, int k_bytes,
+                                       int first, int lane, int wave) {
+    const int mine = DUAL ? N / 2 : N;
 #pragma unroll
-  for (int i = 0; i < LR; ++i) {
-    const int row = (i * TL::waves + wave) * 8 + (lane >> 3);
-    const int src = DUAL ? row / 64 * 32 + row % 32 : row;
-    off[i] = (uint32_t)min(src, p.nr - 1 - r0) * (uint32_t)p.r_ld + piece(i);
-  }
+    for (int i = 0; i < loads; ++i) {
+      const int chunk = i * WAVES + wave, row = chunk * 8 + (lane >> 3), src = DUAL ? row / 64 * 32 + row % 32 : row;
+      // (a load's rows begin at a multiple of 8, so r / 2 % 8 is 4 on its odd chunks and lane / 16)
+      const uint32_t piece = (uint32_t)((lane & 7) ^ ((chunk & 1) * 4 + (lane >> 4))) * 16;
+      off[i] = (uint32_t)min(src, rows - 1 - row0) * (uint32_t)ld + piece;
+    }
+    const uint32_t bytes = (uint32_t)(min(mine, rows - row0) - 1) * (uint32_t)ld + (uint32_t)k_bytes;
+    buf[0] = buffer_of((const uint8_t*)base + (int64_t)row0 * ld, bytes);
+    if constexpr (DUAL) buf[1] = buffer_of((const uint8_t*)base2 + (int64_t)row0 * ld, bytes);
 #pragma unroll
-  for (int i = 0; i < LC; ++i) {
-    const int row = (i * TL::waves + wave) * 8 + (lane >> 3);
-    off[LR + i] = (uint32_t)min(row, p.nc - 1 - c0) * (uint32_t)p.c_ld + piece(i);
+    for (int s = 0; s < 4; ++s)
+      at[s] = (uint32_t)(first * 32 + (lane & 31)) * kStepBytes + (uint32_t)(((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
   }
-  const uint32_t k_bytes = (uint32_t)p.steps * kStepBytes;
-  const uint32_t r_rows = (uint32_t)min(DUAL ? TL::R / 2 : TL::R, p.nr - r0), c_rows = (uint32_t)min(TL::C, p.nc - c0);
-  rs[0] = buffer_of((const uint8_t*)p.r + (int64_t)r0 * p.r_ld, (r_rows - 1) * (uint32_t)p.r_ld + k_bytes);
-  if constexpr (DUAL) rs[1] = buffer_of((const uint8_t*)p.r2 + (int64_t)r0 * p.r_ld, (r_rows - 1) * (uint32_t)p.r_ld + k_bytes);
-  cs = buffer_of((const uint8_t*)p.c + (int64_t)c0 * p.c_ld, (c_rows - 1) * (uint32_t)p.c_ld + k_bytes);
+  __device__ __forceinline__ void fetch(int step, uint32_t lds, int wave) const {
+#pragma unroll
+    for (int i = 0; i < loads; ++i) {
+      const int chunk = i * WAVES + wave;
+      v4u b = buf[0];
+      if constexpr (DUAL) {           // 4 loads of 8 rows make a fragment
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          b[e] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(chunk / 4 & 1 ? buf[1][e] : buf[0][e]));
+      }
+      load_to_lds(b, off[i], (uint32_t)step * kStepBytes, lds + (uint32_t)chunk * 1024);
+    }
+  }
+  __device__ __forceinline__ v4u read(const uint8_t* lds, int s, int f) const {
+    return *(const v4u*)(lds + at[s] + f * 32 * kStepBytes);
+  }
+};
 
-  auto fetch = [&](int step, int stage) {
-    const uint32_t k = (uint32_t)(first + step) * kStepBytes;
-    const uint32_t base = lds0 + (uint32_t)stage * TL::stage_bytes;
+// By columns.
+template <typename T, int N, int F, int WAVES>
+struct ByColumns {
+  static constexpr int loads = N / 8 / WAVES, per = 16 / elem_bytes<T>, pieces = N / per, row_bytes = N * elem_bytes<T>;
+  uint32_t off[loads], at[F];
+  const uint8_t *base, *base2;
+  int64_t ld;
+  int k, joint, lane, left;
+
+  // the place of piece p in row k of LDS
+  static __device__ __forceinline__ int place(int k, int p) {
+    if (is_f32<T>) return pieces >= 16 ? p ^ (k >> 2 & 1) << 3 : p;
+    return pieces >= 16 ? p ^ (k & 3) << 2 : pieces == 8 ? p ^ (k >> 1 & 1) << 2 : p;
+  }
+  __device__ __forceinline__ void init(const void* b, const void* b2, int64_t ld_, int row0, int rows, int k_, int joint_,
+                                       int first, int lane_, int wave) {
+    base = (const uint8_t*)b + (int64_t)row0 * elem_bytes<T>;
+    base2 = b2 ? (const uint8_t*)b2 + (int64_t)row0 * elem_bytes<T> : nullptr;
+    ld = ld_; k = k_; joint = joint_; lane = lane_;
+    left = (rows - row0 + per - 1) / per;           // pieces of a row from here on
 #pragma unroll
-    for (int i = 0; i < LR; ++i) {
-      const int chunk = i * TL::waves + wave;
-      if constexpr (DUAL) {
-        // 4 loads of 8 rows make a fragment; waves are a multiple of 4 or a load's
-        // fragment is its wave's to find
-        v4u b;
+    for (int i = 0; i < loads; ++i) off[i] = offset(i, wave, kStep<T>);
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4)
-          b[k4] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(chunk / 4 & 1 ? rs[1][k4] : rs[0][k4]));
-        load_to_lds(b, off[i], k, base + (uint32_t)chunk * 1024);
+    for (int f = 0; f < F; ++f) {
+      if constexpr (is_f32<T>) {
+        const int row = (first + f) * 32 + (lane & 31), kk = (lane >> 5) * 4;
+        at[f] = (uint32_t)(kk * row_bytes + place(kk, row / 4) * 16 + row % 4 * 4);
       } else {
-        load_to_lds(rs[0], off[i], k, base + (uint32_t)chunk * 1024);
+        const int i = lane & 15, kk = (lane >> 5) * 8 + i / 4, row = (first + f) * 32 + (lane >> 4 & 1) * 16 + i % 4 * 4;
+        at[f] = (uint32_t)(kk * row_bytes + place(kk, row / 8) * 16 + row % 8 * 2);
       }
     }
+  }
+  // of load i from the step's first row of k, of which `rows` are there
+  __device__ __forceinline__ uint32_t offset(int i, int wave, int rows) const {
+    const int slot = (i * WAVES + wave) * 64 + lane, kk = slot / pieces, p = place(kk, slot % pieces);
+    return (uint32_t)min(kk, rows - 1) * (uint32_t)ld + (uint32_t)min(p, left - 1) * 16;
+  }
+  __device__ __forceinline__ void fetch(int step, uint32_t lds, int wave) const {
+    const bool second = base2 && step >= joint;
+    const int k0 = min((second ? step - joint : step) * kStep<T>, k - 1), rows = k - k0;
+    const v4u b = buffer_of((second ? base2 : base) + (int64_t)k0 * ld,
+                            (uint32_t)(min(rows, kStep<T>) - 1) * (uint32_t)ld + (uint32_t)left * 16);
 #pragma unroll
-    for (int i = 0; i < LC; ++i)
-      load_to_lds(cs, off[LR + i], k, base + TL::R * kStepBytes + (uint32_t)(i * TL::waves + wave) * 1024);
+    for (int i = 0; i < loads; ++i) {
+      const uint32_t o = rows < kStep<T> ? offset(i, wave, rows) : off[i];
+      load_to_lds(b, o, 0, lds + (uint32_t)(i * WAVES + wave) * 1024);
+    }
+  }
+  __device__ __forceinline__ v4u read(const uint8_t* lds, int s, int f) const {
+    const uint8_t* p = lds + at[f];
+    if constexpr (is_f32<T>) {
+      v4u v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *(const uint32_t*)(p + (s * 8 + i) * row_bytes);
+      return v;
+    } else {
+      typedef short s4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s4 lds_s4;
+      const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + s * 16 * row_bytes));
+      const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + (s * 16 + 4) * row_bytes));
+      const v2u a = __builtin_bit_cast(v2u, lo), b = __builtin_bit_cast(v2u, hi);
+      return (v4u){a[0], a[1], b[0], b[1]};
+    }
+  }
+};
+
+template <bool C, typename A, typename B> struct Pick { typedef A type; };
+template <typename A, typename B> struct Pick<false, A, B> { typedef B type; };
+
+// The sums of this wave: acc[i][j] of fragment i of R and j of C.
+template <typename T, typename TL, int WR, int WC, int FR, int FC, int NS, Form FORM>
+__device__ __forceinline__ void multiply(const Product& p, const Place& place, uint8_t* lds_raw, v16f (&acc)[FR][FC]) {
+  constexpr bool dual = FORM == DUAL_ROWS, r_rows = FORM == ROWS_ROWS || dual, c_rows = FORM != COLS_COLS;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave % WR, wc = wave / WR;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds_raw;
+  const int first = (int)((int64_t)place.slice * p.steps / p.slices);
+  const int n = (int)((int64_t)(place.slice + 1) * p.steps / p.slices) - first;
+
+  typename Pick<r_rows, ByRows<T, TL::R, FR, TL::waves, dual>, ByColumns<T, TL::R, FR, TL::waves>>::type R;
+  typename Pick<c_rows, ByRows<T, TL::C, FC, TL::waves, false>, ByColumns<T, TL::C, FC, TL::waves>>::type C;
+  if constexpr (r_rows) R.init(p.r, p.r2, p.r_ld, place.r * (dual ? TL::R / 2 : TL::R), p.nr, p.steps * kStepBytes, wr * FR, lane, wave);
+  else R.init(p.r, p.r2, p.r_ld, place.r * TL::R, p.nr, p.k, p.joint, wr * FR, lane, wave);
+  if constexpr (c_rows) C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStepBytes, wc * FC, lane, wave);
+  else C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStep<T>, 0, wc * FC, lane, wave);
+
+  auto fetch = [&](int step, int stage) {
+    const uint32_t base = lds0 + (uint32_t)stage * TL::stage_bytes;
+    R.fetch(first + step, base, wave);
+    C.fetch(first + step, base + TL::R * kStepBytes, wave);
   };
 
 #pragma unroll
   for (int i = 0; i < FR; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j) acc[i][j] = (v16f)(0.0f);
-
-  const int wr = wave % WR, wc = wave / WR;
-  uint32_t at_r[4], at_c[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const uint32_t x = (uint32_t)(lane & 31) * kStepBytes + (uint32_t)(((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
-    at_r[s] = x + (uint32_t)(wr * FR * 32) * kStepBytes;
-    at_c[s] = x + (uint32_t)(TL::R + wc * FC * 32) * kStepBytes;
-  }
 
   // Fragments are read one sub-step ahead of the matrix instructions that use them, and
   // the first of a step before the last instructions of the step before: no wave waits
@@ -195,9 +285,9 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& at, uint
   auto read = [&](int s, int stage) {
     const uint8_t* buf = lds_raw + stage * TL::stage_bytes;
 #pragma unroll
-    for (int i = 0; i < FR; ++i) fr[s & 1][i] = *(const v4u*)(buf + at_r[s] + i * 32 * kStepBytes);
+    for (int i = 0; i < FR; ++i) fr[s & 1][i] = R.read(buf, s, i);
 #pragma unroll
-    for (int j = 0; j < FC; ++j) fc[s & 1][j] = *(const v4u*)(buf + at_c[s] + j * 32 * kStepBytes);
+    for (int j = 0; j < FC; ++j) fc[s & 1][j] = C.read(buf + TL::R * kStepBytes, s, j);
   };
   auto use = [&](int s) {
 #pragma unroll
