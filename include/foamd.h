@@ -531,7 +531,7 @@ int fo_grad_clip(const fo_grad* list, int32_t count, int32_t order, double max_n
 enum fo_loss_reduction { FO_LOSS_NONE = 0, FO_LOSS_MEAN = 1, FO_LOSS_SUM = 2 };
 
 /* Arguments of the linear cross entropy.  Limits: rows 2^21, cols 2^20, vocab
- * 2^24, rows * vocab 2^38. */
+ * 2^24, the product of any two 2^36. */
 typedef struct fo_loss {
   const void*    x;         /* rows x cols */
   const void*    weight;    /* vocab x cols */
@@ -569,14 +569,17 @@ int fo_loss_forward_workspace(const fo_loss* args, int64_t* bytes);
  *   (whose x may hold anything, NaN included)
  *   dx = dz weight;  dweight = dz^T x
  * The logits are computed again, a piece of the vocabulary at a time; a piece's
- * dz is rounded to dtype, f apart.  Rows with an invalid target give NaN.
+ * dz, over the largest |f|, is rounded to dtype (half precision holds it times
+ * 2^15, so it resolves 2^-39).  Rows with an invalid target give NaN, in their
+ * own dx and in dweight.
  */
 int fo_loss_backward(const fo_loss* args, void* stream);
 int fo_loss_backward_workspace(const fo_loss* args, int64_t* bytes);
 
 enum fo_activation { FO_SILU = 0, FO_GELU = 1, FO_GELU_TANH = 2 };
 
-/* Arguments of the gated block.  Limits: rows 2^21, cols and features 2^20. */
+/* Arguments of the gated block.  Limits: rows 2^21, cols and features 2^20, the
+ * product of any two of rows, cols and 2 features 2^36. */
 typedef struct fo_gated {
   const void* x;            /* rows x cols */
   const void* gate;         /* features x cols */
@@ -587,7 +590,7 @@ typedef struct fo_gated {
   const void* dy;           /* backward: rows x features */
   void*       dx;           /* backward: rows x cols (written), or NULL */
   void*       dgate;        /* backward: features x cols (written), or NULL */
-  void*       dup;          /* likewise; both or none */
+  void*       dup;          /* likewise */
   void*       workspace;
   int64_t     workspace_bytes;
   int64_t     rows, cols, features, x_ld, gate_ld, up_ld, dy_ld;

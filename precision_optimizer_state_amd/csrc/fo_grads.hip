@@ -277,15 +277,20 @@ int grad_checks(const fo_grad* list, int32_t count, int32_t order, const float* 
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || bytes < kWorkspace)
     return fail(FO_EINVAL, "the workspace must be 256-byte aligned and hold %lld bytes", (long long)kWorkspace);
   std::vector<Span> spans;
-  spans.reserve(2 * (size_t)count + 2);
+  if (clip) spans.reserve(2 * (size_t)count + 2);
+  const uintptr_t norm_at = reinterpret_cast<uintptr_t>(norm), ws_at = reinterpret_cast<uintptr_t>(workspace);
+  bool sorted = true, scratch = ws_at < norm_at + 4 && norm_at < ws_at + kWorkspace;
   auto add = [&](const void* p, int64_t n, bool out) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     if ((uint64_t)n > UINTPTR_MAX - a) return false;
-    spans.push_back({a, a + (uintptr_t)n, out});
+    const uintptr_t b = a + (uintptr_t)n;
+    scratch |= (a < norm_at + 4 && norm_at < b) || (a < ws_at + kWorkspace && ws_at < b);
+    if (clip) {                               // (what is only read may overlap)
+      sorted &= spans.empty() || spans.back().lo <= a;
+      spans.push_back({a, b, out});
+    }
     return true;
   };
-  add(norm, 4, true);
-  add(workspace, kWorkspace, true);
   *total = 0;
   for (int32_t i = 0; i < count; ++i) {
     const fo_grad& t = list[i];
@@ -310,7 +315,8 @@ int grad_checks(const fo_grad* list, int32_t count, int32_t order, const float* 
     if (!fits) return fail(FO_EINVAL, "tensor %d does not fit the address space", i);
     *total += (t.n + kTile - 1) / kTile;
   }
-  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  if (scratch) return fail(FO_EALIAS, "the norm or the workspace overlaps a tensor of the list, or each other");
+  if (!sorted) std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
   uintptr_t hi_any = 0, hi_out = 0;
   for (const Span& s : spans) {
     if (s.lo < hi_out || (s.out && s.lo < hi_any)) return fail(FO_EALIAS, "arrays of the list overlap at %p", (void*)s.lo);

@@ -37,7 +37,7 @@ template <typename T, typename E, Form F, bool NARROW_OK>
 void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStream_t s) {
   p.tiles_r = c.tiles_r; p.tiles_c = c.tiles_c; p.slices = c.slices;
   if constexpr (NARROW_OK)
-    if (c.kind == NARROW) return launch_tile<T, E, F, 1, 1, 2, 1, 4>(p, e, s);
+    if (c.kind == NARROW) return launch_tile<T, E, F, 1, 1, 2, 1, 3>(p, e, s);
   if (c.kind == WIDE) return launch_tile<T, E, F, 2, 4, 4, 2, 2>(p, e, s);
   if (c.kind == MIDDLE) return launch_tile<T, E, F, 2, 2, 2, 2, 2>(p, e, s);
   launch_tile<T, E, F, 1, 2, 2, 1, 4>(p, e, s);
@@ -78,6 +78,13 @@ Product product_of(const Operand& r, int64_t nr, const Operand& c, int64_t nc, i
 // ---------------------------------------------------------------------------
 // linear cross entropy
 // ---------------------------------------------------------------------------
+int area_check(int64_t rows, int64_t cols, int64_t out) {
+  if (rows * cols > kMaxArea || rows * out > kMaxArea || cols * out > kMaxArea)
+    return fail(FO_EINVAL, "the product of two of the sizes %lld, %lld and %lld is more than 2^36", (long long)rows,
+                (long long)cols, (long long)out);
+  return FO_OK;
+}
+
 int loss_checks(const fo_loss* a) {
   if (!a) return fail(FO_EINVAL, "args is NULL");
   if (!dtype_ok(a->dtype)) return fail(FO_EINVAL, "bad element type %d", a->dtype);
@@ -85,7 +92,7 @@ int loss_checks(const fo_loss* a) {
   if (a->rows < 0 || a->rows > kMaxTokens) return fail(FO_EINVAL, "rows = %lld is not in [0, 2^21]", (long long)a->rows);
   if (a->cols < 1 || a->cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^20]", (long long)a->cols);
   if (a->vocab < 1 || a->vocab > kMaxVocab) return fail(FO_EINVAL, "vocab = %lld is not in [1, 2^24]", (long long)a->vocab);
-  if (a->rows * a->vocab > kMaxLogits) return fail(FO_EINVAL, "rows * vocab is more than 2^38");
+  FO_TRY(area_check(a->rows, a->cols, a->vocab));
   if (!(a->smoothing >= 0.0 && a->smoothing <= 1.0)) return fail(FO_EINVAL, "the smoothing must lie in [0, 1]");
   return FO_OK;
 }
@@ -153,7 +160,7 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
     const Product pz = product_of(w, nv, x, a->rows, b.k, es);
     // tokens in whole steps: the padding is written too (as zeros)
     launch_product<T, LogitGradients, ROWS_ROWS, false>(
-        pz, cut(nv, b.n, pz.steps, false, false, false),
+        pz, cut(a->dtype, nv, b.n, pz.steps, false, false, false),
         {at(ws, b.dz), nvp, a->lse, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
          (float)a->smoothing}, s);
     if (a->dx) {
@@ -164,7 +171,7 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
     if (a->dweight) {
       const Product pw = product_of({at(ws, b.xm), b.k}, a->cols, dz, nv, b.n, es);
       launch_product<T, StoreScaled, COLS_COLS, true>(
-          pw, cut(a->cols, nv, pw.steps, false, true, false),
+          pw, cut(a->dtype, a->cols, nv, pw.steps, false, true, false),
           {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
            1.0f / scale}, s);
     }
@@ -188,6 +195,7 @@ int gated_checks(const fo_gated* a) {
   if (a->cols < 1 || a->cols > kMaxCols) return fail(FO_EINVAL, "cols = %lld is not in [1, 2^20]", (long long)a->cols);
   if (a->features < 1 || a->features > kMaxFeatures)
     return fail(FO_EINVAL, "features = %lld is not in [1, 2^20]", (long long)a->features);
+  FO_TRY(area_check(a->rows, a->cols, 2 * a->features));
   if (!a->g != !a->u) return fail(FO_EINVAL, "g and u go together");
   return FO_OK;
 }
@@ -245,7 +253,7 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
     Product p = product_of(x, a->cols, d, 2 * half, b.n, es);
     p.k = (int)a->rows;
     launch_product<T, StoreScaled, COLS_COLS, true>(
-        p, cut(a->cols, 2 * half, p.steps, false, true, false),
+        p, cut(a->dtype, a->cols, 2 * half, p.steps, false, true, false),
         {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, nullptr, 1.0f}, s);
   }
   return launch_check("gated backward launch");

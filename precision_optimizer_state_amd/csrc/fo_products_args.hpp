@@ -22,7 +22,7 @@ using rows::elem_size;
 constexpr int64_t kMaxRowBytes = int64_t(1) << 23;
 constexpr int64_t kMaxTokens = int64_t(1) << 21, kMaxCols = int64_t(1) << 20, kMaxFeatures = int64_t(1) << 20;
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
-constexpr int64_t kMaxLogits = int64_t(1) << 38;      // tokens * vocab: a launch's threads fit 32 bits
+constexpr int64_t kMaxArea = int64_t(1) << 36;        // of any two of a product's sizes: a launch's threads fit 32 bits
 
 inline int64_t up(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
 inline int64_t padded(int64_t n) { return up(n, 64); }          // whole steps of every type
@@ -53,31 +53,95 @@ constexpr int tile_c(TileKind k) { return k == WIDE ? 256 : k == MIDDLE ? 128 : 
 constexpr int waves_r(TileKind k) { return k == WIDE || k == MIDDLE ? 2 : 1; }
 constexpr int64_t kUnits = 256;                                 // compute units
 
-// nr (with `dual`, of each of two matrices) rows of R against nc of C, `steps` of k.
-inline Cut cut(int64_t nr, int64_t nc, int64_t steps, bool dual, bool narrow_ok, bool sliced) {
+// What a product takes, in microseconds, by the times measured on the card (`steps` of
+// one round: all compute units once).  A round of wide tiles is 256 of them, one per
+// compute unit, of the others 512; a last round of half of that or less takes the second
+// figure of each pair.  16-bit types: 1.67 per step (wide), 0.94 and 0.59 (middle), 0.36
+// and 0.31 (small); float32, whose matrix instructions take 8 times as long, 7.4, 4 and
+// 2, and 1.1 (a small tile's two waves leave half of the matrix units idle).  What a
+// round takes besides its steps differs with the epilogue (4 to 15, 2 to 8 and 3 to 5):
+// its middle is taken.
+inline double round_time(TileKind k, bool f32, bool half, double steps) {
+  const double fixed = k == WIDE ? 9.0 : k == MIDDLE ? 4.5 : 4.0;
+  const double step = f32 ? (k == WIDE ? 7.4 : k == MIDDLE ? (half ? 2.0 : 4.0) : 1.1)
+                          : (k == WIDE ? 1.67 : k == MIDDLE ? (half ? 0.59 : 0.94) : (half ? 0.31 : 0.36));
+  return fixed + step * steps;
+}
+inline double product_time(TileKind k, bool f32, int64_t tiles, int64_t slices, int64_t steps) {
+  const int64_t slots = k == WIDE ? kUnits : 2 * kUnits, n = tiles * slices, last = n % slots;
+  const double each = (double)((steps + slices - 1) / slices);
+  return (double)(n / slots) * round_time(k, f32, false, each) +
+         (last ? round_time(k, f32, k != WIDE && last <= kUnits, each) : 0.0);
+}
+
+// How nr (with `dual`, of each of two matrices) rows of R against nc of C, `steps` of k,
+// are cut: the kind of tile, and with `sliced` the number of slices of k (whose sums are
+// written and read once more, 4 bytes each way at 5 TB/s), that take the least time.
+// Up to 32 rows of C go in narrow tiles, which waste least on rows that are not there.
+inline Cut cut(int dtype, int64_t nr, int64_t nc, int64_t steps, bool dual, bool narrow_ok, bool sliced) {
   const int64_t all_r = dual ? 2 * up(nr, 32) : nr;
-  Cut c = {};
+  const bool f32 = dtype == FO_F32;
   auto tiles = [&](TileKind k) {
-    c.kind = k;
-    c.tiles_r = (int)((all_r + tile_r(k) - 1) / tile_r(k));
-    c.tiles_c = (int)((nc + tile_c(k) - 1) / tile_c(k));
-    return (int64_t)c.tiles_r * c.tiles_c;
+    return Cut{k, (int)((all_r + tile_r(k) - 1) / tile_r(k)), (int)((nc + tile_c(k) - 1) / tile_c(k)), 1};
   };
-  int64_t n;
-  if (narrow_ok && nc <= 32) n = tiles(NARROW);
-  else if ((n = tiles(WIDE)) < kUnits && (n = tiles(MIDDLE)) < kUnits) n = tiles(SMALL);
-  c.slices = 1;
-  if (sliced) c.slices = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kUnits / n, steps / 8, 32}));
-  return c;
+  auto slices = [&](Cut c) {
+    const int64_t n = (int64_t)c.tiles_r * c.tiles_c;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * kUnits / n, steps / 8, 32}));
+  };
+  if (narrow_ok && nc <= 32) {
+    Cut c = tiles(NARROW);
+    if (sliced) c.slices = slices(c);
+    return c;
+  }
+  Cut best = {};
+  double least = 0.0;
+  for (TileKind k : {WIDE, MIDDLE, SMALL}) {
+    Cut c = tiles(k);
+    const int64_t n = (int64_t)c.tiles_r * c.tiles_c;
+    // float32 sums of long k are also cut for their accuracy: chains of at most 2048 terms
+    const int fewest = sliced && f32 ? (int)std::min<int64_t>((steps + 63) / 64, 32) : 1;
+    for (int s = fewest; s <= (sliced ? 32 : 1) && (s == fewest || steps / s >= 8); ++s) {
+      const double t = product_time(k, f32, n, s, steps) + (sliced ? (double)s * (double)nr * (double)nc * 8e-6 / 5.0 : 0.0);
+      if (best.slices && t >= least) continue;
+      best = c;
+      best.slices = s;
+      least = t;
+    }
+  }
+  return best;
+}
+// (the time that cut() expects)
+inline double cut_time(int dtype, const Cut& c, int64_t steps) {
+  return c.kind == NARROW ? 0.0
+                          : product_time(c.kind, dtype == FO_F32, (int64_t)c.tiles_r * c.tiles_c, c.slices, steps);
 }
 
 // Vocabulary per piece of the backward pass: the logits' gradients of a piece are at
-// most about 2^28 elements (512 MB in 16 bits).
+// most about 2^28 elements (512 MB in 16 bits).  Of the sizes down to half of that the
+// one whose three products fill the card's last rounds best (8192 tokens, 768 columns,
+// 50257 places: 21504 instead of 25344, whose weight gradients are 297 wide tiles on 256
+// compute units).
 constexpr int64_t kPieceElems = int64_t(1) << 28;
-inline int64_t piece_vocab(int64_t tokens, int64_t vocab) {
-  const int64_t most = std::max<int64_t>(1024, kPieceElems / padded(tokens));
-  const int64_t pieces = (vocab + most - 1) / most;
-  return std::min(up((vocab + pieces - 1) / pieces, 256), padded(vocab));
+inline int64_t piece_vocab(int dtype, int64_t tokens, int64_t cols, int64_t vocab) {
+  const int64_t es = (int64_t)elem_size(dtype), n = padded(tokens);
+  const int64_t most = std::min(std::max<int64_t>(1024, kPieceElems / n / 256 * 256), kMaxRowBytes / 4);
+  if (vocab <= most) return padded(vocab);
+  const int64_t steps_d = (cols * es + 127) / 128, steps_n = n * es / 128;
+  auto time = [&](int64_t nv) {
+    const int64_t steps_v = padded(nv) * es / 128;
+    return cut_time(dtype, cut(dtype, nv, n, steps_d, false, false, false), steps_d) +
+           cut_time(dtype, cut(dtype, cols, tokens, steps_v, false, true, true), steps_v) +
+           cut_time(dtype, cut(dtype, cols, nv, steps_n, false, true, false), steps_n);
+  };
+  int64_t best = most;
+  double least = 0.0;
+  for (int64_t nv = most; 2 * nv >= most && nv >= 1024; nv -= std::max<int64_t>(256, most / 32 / 256 * 256)) {
+    const double t = (double)(vocab / nv) * time(nv) + (vocab % nv ? time(vocab % nv) : 0.0);
+    if (nv != most && t >= least) continue;
+    best = nv;
+    least = t;
+  }
+  return best;
 }
 
 // What a loss call's workspace holds (offsets; -1: not there).
@@ -93,7 +157,7 @@ inline LossForward loss_forward(const fo_loss* a) {
   f.k = a->cols % (128 / es) ? padded(a->cols) : a->cols;
   if (!direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) f.x = l.take(a->rows * f.k * es);
   if (!direct(a->weight, a->vocab, a->cols, a->weight_ld, a->dtype)) f.w = l.take(a->vocab * f.k * es);
-  f.c = cut(a->vocab, a->rows, f.k * es / 128, false, true, false);
+  f.c = cut(a->dtype, a->vocab, a->rows, f.k * es / 128, false, true, false);
   const int64_t parts = (int64_t)waves_r(f.c.kind) * f.c.tiles_r;
   f.part = l.take(parts * a->rows * 8);
   if (a->smoothing != 0.0) f.sums = l.take(parts * a->rows * 4);
@@ -114,7 +178,7 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   const int64_t es = (int64_t)elem_size(a->dtype);
   b.k = a->cols % (128 / es) ? padded(a->cols) : a->cols;
   b.n = padded(a->rows);
-  b.piece = piece_vocab(a->rows, a->vocab);
+  b.piece = piece_vocab(a->dtype, a->rows, a->cols, a->vocab);
   b.unit = l.take(a->rows * 4);
   b.factor = l.take(4);
   if (!direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) b.x = l.take(a->rows * b.k * es);
@@ -123,7 +187,7 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   b.dz = l.take(b.n * b.piece * es);
   b.sums_ld = up(a->cols, 4);
   if (dx) {
-    b.dx = cut(a->cols, a->rows, b.piece * es / 128, false, true, true);
+    b.dx = cut(a->dtype, a->cols, a->rows, b.piece * es / 128, false, true, true);
     b.sums = l.take((int64_t)b.dx.slices * a->rows * b.sums_ld * 4);
   }
   b.bytes = l.bytes;
@@ -143,7 +207,7 @@ inline GatedForward gated_forward(const fo_gated* a) {
     f.gate = l.take(a->features * f.k * es);
     f.up = l.take(a->features * f.k * es);
   }
-  f.c = cut(a->features, a->rows, f.k * es / 128, true, true, false);
+  f.c = cut(a->dtype, a->features, a->rows, f.k * es / 128, true, true, false);
   f.bytes = l.bytes;
   return f;
 }
@@ -168,7 +232,7 @@ inline GatedBackward gated_backward(const fo_gated* a, bool dx, bool dw) {
       b.gate = l.take(a->features * b.k * es);
       b.up = l.take(a->features * b.k * es);
     }
-    b.dx = cut(a->cols, a->rows, 2 * b.half * es / 128, false, true, true);
+    b.dx = cut(a->dtype, a->cols, a->rows, 2 * b.half * es / 128, false, true, true);
     if (b.dx.slices > 1) b.sums = l.take((int64_t)b.dx.slices * a->rows * b.sums_ld * 4);
   }
   if (dw && !direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) b.x = l.take(a->rows * b.k * es);

@@ -257,10 +257,15 @@ Tensor gated_linear(const Tensor& x, const Tensor& gate, const Tensor& up, int64
 // ---------------------------------------------------------------------------
 // gradients
 // ---------------------------------------------------------------------------
-void check_grad(const Tensor& g) {
+// (check_device asks for the current device; a list's tensors ask once)
+void check_grad(const Tensor& g, c10::DeviceIndex device) {
   TORCH_CHECK_VALUE(g.defined() && g.layout() == at::kStrided, "gradients must be dense tensors");
-  check_device(g);
+  if (!g.is_cuda() || g.device().index() != device) check_device(g);
   dtype_of(g);
+}
+// The current device, or that of a tensor off the GPU, whose check then says so.
+c10::DeviceIndex device_of(const std::vector<Tensor>& list) {
+  return list.empty() || !list[0].defined() || !list[0].is_cuda() ? c10::DeviceIndex(-1) : c10::hip::current_device();
 }
 
 // Whether a tensor's elements are one stretch of memory, in whatever order.
@@ -280,9 +285,10 @@ Tensor grad_norm(const std::vector<Tensor>& grads, int64_t order) {
   check_plain({});
   std::vector<fo_grad> list(grads.size());
   std::vector<Tensor> held;
+  const auto device = device_of(grads);
   for (size_t i = 0; i < grads.size(); ++i) {
     const Tensor& g = grads[i];
-    check_grad(g);
+    check_grad(g, device);
     const Tensor* t = &g;
     if (!flat(g)) t = &held.emplace_back(resolved(g.detach()).contiguous());
     list[i] = {t->data_ptr(), nullptr, t->numel(), dtype_of(g), 0};
@@ -303,10 +309,11 @@ Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>& outs, d
   std::vector<fo_grad> list(grads.size());
   std::vector<Tensor> held;
   std::vector<std::pair<Tensor, Tensor>> back;          // copies to write back
+  const auto device = device_of(grads);
   for (size_t i = 0; i < grads.size(); ++i) {
     const Tensor &g = grads[i], &o = outs[i];
-    check_grad(g);
-    check_grad(o);
+    check_grad(g, device);
+    if (!g.is_same(o)) check_grad(o, device);
     TORCH_CHECK_VALUE(g.sizes() == o.sizes(), "a gradient of shape ", sizes(g), " is clipped into ", sizes(o));
     const bool in_place = g.is_same(o);
     const bool direct = flat(g) && flat(o) && g.strides() == o.strides();
