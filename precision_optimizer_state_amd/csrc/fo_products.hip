@@ -283,9 +283,9 @@ int fo_loss_forward(const fo_loss* a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!any) {
     FO_TRY(ar.disjoint());
-    if (reduced)
-      hipLaunchKernelGGL(k_loss_sum, 1, 1024, 0, s, (const float*)nullptr, a->target, a->ignore_index, 0,
-                         (int)(a->reduction == FO_LOSS_MEAN), a->loss, a->count);
+    if (!reduced) return FO_OK;
+    hipLaunchKernelGGL(k_loss_sum, 1, 1024, 0, s, (const float*)nullptr, a->target, a->ignore_index, 0,
+                       (int)(a->reduction == FO_LOSS_MEAN), a->loss, a->count);
     return launch_check("loss forward launch");
   }
   const LossForward f = loss_forward(a);
@@ -317,15 +317,13 @@ int fo_loss_backward(const fo_loss* a, void* stream) {
   FO_TRY(ar.add(a->dx, "dx", true, false, a->rows, a->cols, a->cols, es));
   FO_TRY(ar.add(a->dweight, "dweight", true, false, a->vocab, a->cols, a->cols, es));
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((!a->dx || !any) && !a->dweight) return ar.disjoint();
   if (!any) {
     FO_TRY(ar.disjoint());
-    if (a->dweight) {
-      const int64_t words = a->vocab * a->cols;
-      hipLaunchKernelGGL(k_zero, grid_of((words * (int64_t)es + 4095) / 4096), 256, 0, s, a->dweight, words * (int64_t)es);
-    }
+    const int64_t bytes = a->vocab * a->cols * (int64_t)es;
+    hipLaunchKernelGGL(k_zero, grid_of((bytes + 4095) / 4096), 256, 0, s, a->dweight, bytes);
     return launch_check("loss backward launch");
   }
-  if (!a->dx && !a->dweight) return FO_OK;
   const LossBackward b = loss_backward(a, a->dx, a->dweight);
   FO_TRY(workspace_check(a->workspace, a->workspace_bytes, b.bytes, ar));
   FO_TRY(ar.disjoint());
@@ -348,7 +346,7 @@ int fo_gated_forward(const fo_gated* a, void* stream) {
   Arrays ar;
   FO_TRY(gated_inputs(a, ar, false));
   FO_TRY(ar.add(a->y, "y", true, a->rows > 0, a->rows, a->features, a->features, elem_size(a->dtype)));
-  if (a->rows == 0) return FO_OK;
+  if (a->rows == 0) return ar.disjoint();
   const GatedForward f = gated_forward(a);
   FO_TRY(workspace_check(a->workspace, a->workspace_bytes, f.bytes, ar));
   FO_TRY(ar.disjoint());
@@ -377,6 +375,7 @@ int fo_gated_backward(const fo_gated* a, void* stream) {
   FO_TRY(ar.add(a->dgate, "dgate", true, false, a->features, a->cols, a->cols, es));
   FO_TRY(ar.add(a->dup, "dup", true, false, a->features, a->cols, a->cols, es));
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((!a->dx || a->rows == 0) && !a->dgate && !a->dup) return ar.disjoint();
   if (a->rows == 0) {
     FO_TRY(ar.disjoint());
     const int64_t bytes = a->features * a->cols * (int64_t)es;
@@ -384,7 +383,6 @@ int fo_gated_backward(const fo_gated* a, void* stream) {
       if (out) hipLaunchKernelGGL(k_zero, grid_of((bytes + 4095) / 4096), 256, 0, s, out, bytes);
     return launch_check("gated backward launch");
   }
-  if (!a->dx && !a->dgate && !a->dup) return FO_OK;
   const GatedBackward b = gated_backward(a, a->dx, a->dgate || a->dup);
   FO_TRY(workspace_check(a->workspace, a->workspace_bytes, b.bytes, ar));
   FO_TRY(ar.disjoint());

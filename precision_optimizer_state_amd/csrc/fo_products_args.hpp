@@ -84,9 +84,11 @@ inline Cut cut(int dtype, int64_t nr, int64_t nc, int64_t steps, bool dual, bool
   auto tiles = [&](TileKind k) {
     return Cut{k, (int)((all_r + tile_r(k) - 1) / tile_r(k)), (int)((nc + tile_c(k) - 1) / tile_c(k)), 1};
   };
+  // at most 32, and 1 GB of sums
+  const int64_t most = sliced ? std::max<int64_t>(1, std::min<int64_t>(32, (int64_t(1) << 28) / (nr * nc))) : 1;
   auto slices = [&](Cut c) {
     const int64_t n = (int64_t)c.tiles_r * c.tiles_c;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * kUnits / n, steps / 8, 32}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * kUnits / n, steps / 8, most}));
   };
   if (narrow_ok && nc <= 32) {
     Cut c = tiles(NARROW);
@@ -99,8 +101,8 @@ inline Cut cut(int dtype, int64_t nr, int64_t nc, int64_t steps, bool dual, bool
     Cut c = tiles(k);
     const int64_t n = (int64_t)c.tiles_r * c.tiles_c;
     // float32 sums of long k are also cut for their accuracy: chains of at most 2048 terms
-    const int fewest = sliced && f32 ? (int)std::min<int64_t>((steps + 63) / 64, 32) : 1;
-    for (int s = fewest; s <= (sliced ? 32 : 1) && (s == fewest || steps / s >= 8); ++s) {
+    const int fewest = f32 ? (int)std::min((steps + 63) / 64, most) : 1;
+    for (int s = fewest; s <= most && (s == fewest || steps / s >= 8); ++s) {
       const double t = product_time(k, f32, n, s, steps) + (sliced ? (double)s * (double)nr * (double)nc * 8e-6 / 5.0 : 0.0);
       if (best.slices && t >= least) continue;
       best = c;
