@@ -140,11 +140,14 @@ template <typename T>
 int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
   void* ws = a->workspace;
-  float *unit = (float*)at(ws, b.unit), *factor = (float*)at(ws, b.factor);
-  const bool none = a->reduction == FO_LOSS_NONE;
-  hipLaunchKernelGGL(k_loss_factors, 1, 1024, 0, s, a->dloss, none ? a->dloss_ld : (int64_t)0,
-                     a->reduction == FO_LOSS_MEAN ? (const float*)a->count : (const float*)nullptr, a->target, a->ignore_index,
-                     (int)a->rows, unit, factor);
+  // a token's gradient is a common factor times its unit: 1 with a reduction
+  float *unit = (float*)at(ws, b.unit), *largest = (float*)at(ws, b.factor);
+  Factor factor = {a->dloss, a->reduction == FO_LOSS_MEAN ? a->count : nullptr};
+  if (unit) {
+    hipLaunchKernelGGL(k_loss_factors, 1, 1024, 0, s, a->dloss, a->dloss_ld, a->target, a->ignore_index, (int)a->rows, unit,
+                       largest);
+    factor = {largest, nullptr};
+  }
   const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, ws, b.x, b.k, s);
   // dweight reads x without the tokens that are not counted: 0 times what they hold need not be 0
   if (a->dweight)
@@ -166,17 +169,21 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
     if (a->dx) {
       Product px = product_of(w, a->cols, dz, a->rows, nvp, es);
       px.k = (int)nv;
-      launch_product<T, KeepSums, COLS_ROWS, true>(px, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
+      if (b.sums >= 0)
+        launch_product<T, KeepSums, COLS_ROWS, true>(px, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
+      else
+        launch_product<T, StoreScaled, COLS_ROWS, true>(
+            px, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, factor, 1.0f / scale, a->target, a->ignore_index}, s);
     }
     if (a->dweight) {
       const Product pw = product_of({at(ws, b.xm), b.k}, a->cols, dz, nv, b.n, es);
       launch_product<T, StoreScaled, COLS_COLS, true>(
           pw, cut(a->dtype, a->cols, nv, pw.steps, false, true, false),
           {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
-           1.0f / scale}, s);
+           1.0f / scale, nullptr, 0}, s);
     }
   }
-  if (a->dx) {
+  if (a->dx && b.sums >= 0) {
     const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.dx.slices, a->dx, factor, a->target,
                         a->ignore_index, (int)a->rows, (int)a->cols, 1.0f / scale};
     hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
@@ -241,11 +248,11 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
     if (b.dx.slices > 1) {
       const int64_t slice = a->rows * b.sums_ld;
       launch_product<T, KeepSums, COLS_ROWS, true>(p, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, 0}, s);
-      const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.dx.slices, a->dx, nullptr, nullptr, 0,
+      const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.dx.slices, a->dx, {nullptr, nullptr}, nullptr, 0,
                           (int)a->rows, (int)a->cols, 1.0f};
       hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
     } else {
-      launch_product<T, StoreScaled, COLS_ROWS, true>(p, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, nullptr, 1.0f}, s);
+      launch_product<T, StoreScaled, COLS_ROWS, true>(p, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, {nullptr, nullptr}, 1.0f, nullptr, 0}, s);
     }
   }
   if (a->dgate || a->dup) {
@@ -254,7 +261,7 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
     p.k = (int)a->rows;
     launch_product<T, StoreScaled, COLS_COLS, true>(
         p, cut(a->dtype, a->cols, 2 * half, p.steps, false, true, false),
-        {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, nullptr, 1.0f}, s);
+        {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, {nullptr, nullptr}, 1.0f, nullptr, 0}, s);
   }
   return launch_check("gated backward launch");
 }

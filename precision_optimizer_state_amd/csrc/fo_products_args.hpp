@@ -137,7 +137,7 @@ inline int64_t piece_vocab(int dtype, int64_t tokens, int64_t cols, int64_t voca
   };
   int64_t best = most;
   double least = 0.0;
-  for (int64_t nv = most; 2 * nv >= most && nv >= 1024; nv -= std::max<int64_t>(256, most / 32 / 256 * 256)) {
+  for (int64_t nv = most; 2 * nv >= most && nv >= 1024; nv -= std::max<int64_t>(256, most / 16 / 256 * 256)) {
     const double t = (double)(vocab / nv) * time(nv) + (vocab % nv ? time(vocab % nv) : 0.0);
     if (nv != most && t >= least) continue;
     best = nv;
@@ -170,7 +170,7 @@ inline LossForward loss_forward(const fo_loss* a) {
 }
 
 struct LossBackward {
-  int64_t unit, factor, x = -1, w = -1, xm = -1, dz = -1, sums = -1, bytes = 0;
+  int64_t unit = -1, factor = -1, x = -1, w = -1, xm = -1, dz = -1, sums = -1, bytes = 0;
   int64_t k, n, piece, sums_ld;                                 // columns and tokens in whole steps; vocabulary per piece
   Cut dx = {};                                                  // of a whole piece
 };
@@ -181,8 +181,10 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   b.k = a->cols % (128 / es) ? padded(a->cols) : a->cols;
   b.n = padded(a->rows);
   b.piece = piece_vocab(a->dtype, a->rows, a->cols, a->vocab);
-  b.unit = l.take(a->rows * 4);
-  b.factor = l.take(4);
+  if (a->reduction == FO_LOSS_NONE) {
+    b.unit = l.take(a->rows * 4);
+    b.factor = l.take(4);
+  }
   if (!direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) b.x = l.take(a->rows * b.k * es);
   if (!direct(a->weight, a->vocab, a->cols, a->weight_ld, a->dtype)) b.w = l.take(std::min(b.piece, a->vocab) * b.k * es);
   if (dw) b.xm = l.take(b.n * b.k * es);
@@ -190,7 +192,7 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   b.sums_ld = up(a->cols, 4);
   if (dx) {
     b.dx = cut(a->dtype, a->cols, a->rows, b.piece * es / 128, false, true, true);
-    b.sums = l.take((int64_t)b.dx.slices * a->rows * b.sums_ld * 4);
+    if (b.dx.slices > 1 || a->vocab > b.piece) b.sums = l.take((int64_t)b.dx.slices * a->rows * b.sums_ld * 4);
   }
   b.bytes = l.bytes;
   return b;
