@@ -262,6 +262,14 @@ void check_grad(const Tensor& g, c10::DeviceIndex device) {
   TORCH_CHECK_VALUE(g.defined() && g.layout() == at::kStrided, "gradients must be dense tensors");
   if (!g.is_cuda() || g.device().index() != device) check_device(g);
   dtype_of(g);
+  TORCH_CHECK_NOT_IMPLEMENTED(!g._fw_grad(/*level=*/0).defined(), "the " FO_OPERATORS " have no forward-mode derivatives");
+}
+// The norm, whose derivatives by tensors of a graph are not provided.
+Tensor as_result(const Tensor& norm, const std::vector<Tensor>& grads) {
+  bool graph = false;
+  for (const Tensor& g : grads) graph |= g.requires_grad();
+  if (!graph) return norm;
+  return without_derivative({norm}, "the norm of gradients has no derivative")[0];
 }
 // The current device, or that of a tensor off the GPU, whose check then says so.
 c10::DeviceIndex device_of(const std::vector<Tensor>& list) {
@@ -298,7 +306,7 @@ Tensor grad_norm(const std::vector<Tensor>& grads, int64_t order) {
   const Workspace ws = grad_workspace();
   check(fo_grad_norm(list.data(), static_cast<int32_t>(list.size()), static_cast<int32_t>(order),
                      static_cast<float*>(norm.data_ptr()), ws.ptr(), ws.bytes, current_stream()));
-  return norm;
+  return as_result(norm, grads);
 }
 
 // Clips `grads` into `outs` (the same tensors: in place); the norm.

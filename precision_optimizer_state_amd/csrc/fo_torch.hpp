@@ -145,22 +145,25 @@ Tensor packed(const Tensor& t) { return t.defined() ? resolved(t).contiguous() :
 
 Tensor empty_like_shape(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
-// Gradients carry no graph of their own: a second differentiation through them
-// fails instead of leaving this operator's part out.
-variable_list once(variable_list grads) {
-  if (!at::GradMode::is_enabled()) return grads;
+// Results that carry no graph of their own: a differentiation through them fails,
+// instead of leaving this operator's part out.
+variable_list without_derivative(variable_list results, const char* why) {
+  if (!at::GradMode::is_enabled()) return results;
   variable_list defined;
-  for (const auto& g : grads)
+  for (const auto& g : results)
     if (g.defined()) defined.push_back(g.detach());
-  if (defined.empty()) return grads;
+  if (defined.empty()) return results;
   for (auto& g : defined) g.requires_grad_(true);
-  const auto error = std::make_shared<torch::autograd::DelayedError>("the " FO_OPERATORS " have no second derivatives",
-                                                                     static_cast<int64_t>(defined.size()));
+  const auto error = std::make_shared<torch::autograd::DelayedError>(why, static_cast<int64_t>(defined.size()));
   const variable_list out = (*error)(std::move(defined));
   size_t i = 0;
-  for (auto& g : grads)
+  for (auto& g : results)
     if (g.defined()) g = out[i++];
-  return grads;
+  return results;
+}
+// ... the gradients of a backward pass
+variable_list once(variable_list grads) {
+  return without_derivative(std::move(grads), "the " FO_OPERATORS " have no second derivatives");
 }
 
 // FoError, raised with (code, message); call once in a module's definition.

@@ -52,7 +52,8 @@ def _listed(tensors) -> list:
 def grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
     """The norm of all elements of `grads` (a tensor or an iterable of them, of
     bfloat16, float16 or float32, mixed or not) as one vector: a float32 scalar
-    on the GPU.  norm_type: 2, 1 or inf.  An empty list has norm 0."""
+    on the GPU.  norm_type: 2, 1 or inf.  An empty list has norm 0.  The norm has no
+    derivatives: a backward pass through it is refused."""
     return _step_ext().grad_norm(_listed(grads), _order(norm_type))
 
 

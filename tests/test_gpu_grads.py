@@ -243,6 +243,27 @@ def test_a_graph_that_saved_a_clipped_gradient_is_refused():
         y.backward()
 
 
+def test_the_norm_has_no_derivative():
+    w = torch.randn(10, device="cuda", requires_grad=True)
+    norm = grad_norm([w, torch.ones(3, device="cuda")])
+    assert abs(float(norm.detach()) - float((w.detach().square().sum() + 3).sqrt())) < 1e-5
+    with pytest.raises(RuntimeError, match="no derivative"):
+        norm.backward()
+    with torch.no_grad():
+        assert not grad_norm([w]).requires_grad
+    assert not grad_norm([w.detach()]).requires_grad
+    with torch.autograd.forward_ad.dual_level(), pytest.raises(NotImplementedError, match="forward-mode"):
+        grad_norm([torch.autograd.forward_ad.make_dual(w.detach(), w.detach())])
+
+
+def test_tracers_are_refused():
+    from torch.fx.experimental.proxy_tensor import make_fx
+    g = torch.randn(10, device="cuda")
+    for f in (lambda t: grad_norm([t]), lambda t: clip_grads([t], 1.0)[1]):
+        with pytest.raises(NotImplementedError, match="traced"):
+            make_fx(f)(g)
+
+
 def test_nothing_behind_the_norm_is_written():
     gs = make([100, 5], "f32", 10)
     norm = torch.full((3,), 7.0, device="cuda")

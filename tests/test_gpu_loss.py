@@ -151,6 +151,41 @@ def test_logits_of_minus_infinity_and_of_the_types_lowest(dtype):
     assert nn.linear_cross_entropy(x, v, t, reduction="none").isnan().all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e5, 1e9, 1e30])
+def test_logits_past_the_integers_of_float32(scale, dtype):
+    """Logits whose product with log2(e) rounds by more than exponentials can take: the
+    probabilities of an exact tie are halves, other places have none."""
+    x = torch.full((40, 64), scale, device="cuda", dtype=TYPES[dtype])
+    w = torch.zeros(300, 64, device="cuda", dtype=TYPES[dtype])
+    w[:, 0] = torch.linspace(-0.5, 0.5, 300, device="cuda").to(w.dtype)
+    w[7, 0], w[205, 0] = 1.0, 1.0
+    t = torch.full((40,), 7, device="cuda")
+    t[1] = 3
+    loss, dx, dw, _ = run(x, w, t, "none")
+    z = float(x[0, 0])
+    ulp = z * 2.0 ** -23                                # the logits' own spacing, or less
+    assert (loss[2:] >= -ulp).all() and (loss[2:] <= ulp + 1).all()
+    assert abs(float(loss[1]) - 1.5 * z) < 0.02 * z + 2
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    # softmax is a half at places 7 and 205, within e to the spacing's power
+    if ulp < 0.01:
+        check("dx", dx[2:, 0], torch.zeros(38, device="cuda"), 1e-2)
+        check("dw", dw[205], 40 * 0.5 * x[0].double(), 0.02 * 40 * 0.5 * x[0].double())
+
+
+def test_an_infinite_gradient_of_one_token():
+    x, w, t = make(21, 30, 64, 90, "bf16")
+    dloss = torch.ones(30, device="cuda")
+    want = run(x, w, t, "none", dloss=dloss)
+    for bad in (float("inf"), float("nan")):
+        dloss[4] = bad
+        _, dx, dw, _ = run(x, w, t, "none", dloss=dloss)
+        keep = torch.arange(30, device="cuda") != 4
+        assert torch.equal(dx[keep], want[1][keep]) and not torch.isfinite(dx[4]).any()
+        assert not torch.isfinite(dw).any()
+
+
 def test_large_logits_neither_overflow_nor_vanish():
     x, w, t = make(12, 40, 64, 300, "f32")
     x = x * 3000.0                                      # logits of tens of thousands

@@ -246,6 +246,37 @@ def test_two_streams_at_once():
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
 
 
+def test_tracers_are_refused():
+    from torch.fx.experimental.proxy_tensor import make_fx
+    x, w = normal(generator(12), 5, 64), normal(generator(13), 70, 64)
+    t = torch.zeros(5, dtype=torch.int64, device="cuda")
+    for f in (lambda a: nn.linear_cross_entropy(a, w, t), lambda a: nn.gated_linear(a, w, w)):
+        for pre in (False, True):
+            with pytest.raises(NotImplementedError, match="traced"):
+                make_fx(f, pre_dispatch=pre)(x)
+        with pytest.raises(NotImplementedError, match="traced"):
+            torch.jit.trace(f, x, check_trace=False)
+        a = x.clone().requires_grad_(True)
+        y = f(a)
+        with pytest.raises(NotImplementedError, match="traced"):
+            make_fx(lambda dy: torch.autograd.grad(y, a, dy, retain_graph=True)[0])(torch.ones_like(y))
+
+
+def test_negated_views():
+    gen = generator(14)
+    x, w, u = normal(gen, 20, 64), normal(gen, 70, 64), normal(gen, 70, 64)
+    t = torch.randint(70, (20,), generator=gen, device="cuda")
+    neg = [torch._neg_view(-a) for a in (x, w, u)]
+    assert torch.equal(nn.linear_cross_entropy(neg[0], neg[1], t), nn.linear_cross_entropy(x, w, t))
+    assert torch.equal(nn.linear_cross_entropy(x, w, torch._neg_view(-t)), nn.linear_cross_entropy(x, w, t))
+    assert torch.equal(nn.gated_linear(*neg), nn.gated_linear(x, w, u))
+    a = x.clone().requires_grad_(True)
+    dy = normal(gen, 20, 70)
+    y = nn.gated_linear(a, w, u)
+    plain = torch.autograd.grad(y, a, dy, retain_graph=True)[0]
+    assert torch.equal(torch.autograd.grad(y, a, torch._neg_view(-dy))[0], plain)
+
+
 def test_inference_mode():
     gen = generator(11)
     x, w = normal(gen, 5, 64), normal(gen, 70, 64)
