@@ -45,25 +45,38 @@ void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStrea
 
 uint8_t* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : static_cast<uint8_t*>(workspace) + offset; }
 
-// dst: dst_rows rows of dst_ld elements
-void pack(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t dst_ld, int64_t dst_rows,
-          const int64_t* target, int64_t ignore, hipStream_t s) {
-  const int64_t es = (int64_t)elem_size(dtype);
-  const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (rows == 1 || ld * es % 16 == 0);
-  const PackArgs a = {src, ld, dst, dst_ld, (int)rows, (int)cols, (int)dst_rows, wide, target, ignore};
-  const unsigned groups = grid_of((dst_rows * dst_ld * es / 16 + 511) / 512);
-  if (dtype == FO_F32) hipLaunchKernelGGL(k_pack<uint32_t>, groups, 256, 0, s, a);
-  else hipLaunchKernelGGL(k_pack<uint16_t>, groups, 256, 0, s, a);
-}
-
 // An operand as its product reads it: the caller's rows, or a copy in the workspace.
 struct Operand { const void* p; int64_t ld; };
-Operand operand(int dtype, const void* src, int64_t ld, int64_t rows, int64_t cols, void* workspace, int64_t offset, int64_t k,
-                hipStream_t s) {
-  if (offset < 0) return {src, ld};
-  pack(dtype, src, ld, rows, cols, at(workspace, offset), k, rows, nullptr, 0, s);
-  return {at(workspace, offset), k};
-}
+
+// The copies that a call needs, made by one launch.
+struct Packing {
+  int dtype;
+  void* workspace;
+  PackJobs jobs = {};
+  int n = 0;
+  int64_t most = 0;
+
+  // rows x cols elements into dst_rows rows of `k` elements at `offset`
+  Operand copy(const void* src, int64_t ld, int64_t rows, int64_t cols, int64_t offset, int64_t k, int64_t dst_rows,
+               const int64_t* target = nullptr, int64_t ignore = 0) {
+    const int64_t es = (int64_t)elem_size(dtype);
+    const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (rows == 1 || ld * es % 16 == 0);
+    jobs.job[n++] = {src, ld, at(workspace, offset), k, (int)rows, (int)cols, (int)dst_rows, wide, target, ignore};
+    most = std::max(most, dst_rows * k * es / 16);
+    return {at(workspace, offset), k};
+  }
+  Operand operand(const void* src, int64_t ld, int64_t rows, int64_t cols, int64_t offset, int64_t k) {
+    return offset < 0 ? Operand{src, ld} : copy(src, ld, rows, cols, offset, k, rows);
+  }
+  void launch(hipStream_t s) {
+    if (!n) return;
+    const dim3 groups(grid_of((most + 511) / 512), (unsigned)n);
+    if (dtype == FO_F32) hipLaunchKernelGGL(k_pack<uint32_t>, groups, 256, 0, s, jobs);
+    else hipLaunchKernelGGL(k_pack<uint16_t>, groups, 256, 0, s, jobs);
+    n = 0;
+    most = 0;
+  }
+};
 
 Product product_of(const Operand& r, int64_t nr, const Operand& c, int64_t nc, int64_t k, int64_t es) {
   Product p = {};
@@ -116,8 +129,10 @@ int workspace_check(void* workspace, int64_t have, int64_t need, Arrays& ar) {
 template <typename T>
 int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
-  const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, a->workspace, f.x, f.k, s);
-  const Operand w = operand(a->dtype, a->weight, a->weight_ld, a->vocab, a->cols, a->workspace, f.w, f.k, s);
+  Packing pack = {a->dtype, a->workspace};
+  const Operand x = pack.operand(a->x, a->x_ld, a->rows, a->cols, f.x, f.k);
+  const Operand w = pack.operand(a->weight, a->weight_ld, a->vocab, a->cols, f.w, f.k);
+  pack.launch(s);
   const bool reduced = a->reduction != FO_LOSS_NONE;
   v2f* part = (v2f*)at(a->workspace, f.part);
   float* sums = (float*)at(a->workspace, f.sums);
@@ -148,17 +163,19 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
                        largest);
     factor = {largest, nullptr};
   }
-  const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, ws, b.x, b.k, s);
+  Packing pack = {a->dtype, ws};
+  const Operand x = pack.operand(a->x, a->x_ld, a->rows, a->cols, b.x, b.k);
   // dweight reads x without the tokens that are not counted: 0 times what they hold need not be 0
-  if (a->dweight)
-    pack(a->dtype, a->x, a->x_ld, a->rows, a->cols, at(ws, b.xm), b.k, b.n, a->target, a->ignore_index, s);
+  Operand xm = {};
+  if (a->dweight) xm = pack.copy(a->x, a->x_ld, a->rows, a->cols, b.xm, b.k, b.n, a->target, a->ignore_index);
   // half precision holds gradients of logits times 2^15
   const float scale = __is_same(T, Fp16) ? 32768.0f : 1.0f;
   const int64_t slice = a->rows * b.sums_ld;
   for (int64_t first = 0; first < a->vocab; first += b.piece) {
     const int64_t nv = std::min(b.piece, a->vocab - first), nvp = padded(nv);
-    const Operand w = operand(a->dtype, static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es, a->weight_ld, nv,
-                              a->cols, ws, b.w, b.k, s);
+    const Operand w = pack.operand(static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es, a->weight_ld, nv,
+                                   a->cols, b.w, b.k);
+    pack.launch(s);
     const Operand dz = {at(ws, b.dz), nvp};
     const Product pz = product_of(w, nv, x, a->rows, b.k, es);
     // tokens in whole steps: the padding is written too (as zeros)
@@ -176,7 +193,7 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
             px, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, factor, 1.0f / scale, a->target, a->ignore_index}, s);
     }
     if (a->dweight) {
-      const Product pw = product_of({at(ws, b.xm), b.k}, a->cols, dz, nv, b.n, es);
+      const Product pw = product_of(xm, a->cols, dz, nv, b.n, es);
       launch_product<T, StoreScaled, COLS_COLS, true>(
           pw, cut(a->dtype, a->cols, nv, pw.steps, false, true, false),
           {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
@@ -221,9 +238,11 @@ int gated_inputs(const fo_gated* a, Arrays& ar, bool backward) {
 template <typename T>
 int run_gated_forward(const fo_gated* a, const GatedForward& f, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
-  const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, a->workspace, f.x, f.k, s);
-  const Operand gate = operand(a->dtype, a->gate, a->gate_ld, a->features, a->cols, a->workspace, f.gate, f.k, s);
-  const Operand up_w = operand(a->dtype, a->up, a->up_ld, a->features, a->cols, a->workspace, f.up, f.k, s);
+  Packing pack = {a->dtype, a->workspace};
+  const Operand x = pack.operand(a->x, a->x_ld, a->rows, a->cols, f.x, f.k);
+  const Operand gate = pack.operand(a->gate, a->gate_ld, a->features, a->cols, f.gate, f.k);
+  const Operand up_w = pack.operand(a->up, a->up_ld, a->features, a->cols, f.up, f.k);
+  pack.launch(s);
   Product p = product_of(gate, a->features, x, a->rows, f.k, es);
   p.r2 = up_w.p;
   launch_product<T, Gated, DUAL_ROWS, true>(p, f.c, {a->y, a->g, a->u, a->activation}, s);
@@ -238,9 +257,12 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
                       a->activation};
   hipLaunchKernelGGL((k_gated_bwd<T>), grid_of((b.n * half / 8 + 255) / 256), 256, 0, s, g);
   const Operand d = {at(ws, b.d), 2 * half};
+  Packing pack = {a->dtype, ws};
+  const Operand gate = pack.operand(a->gate, a->gate_ld, a->features, a->cols, b.gate, b.k);
+  const Operand up_w = pack.operand(a->up, a->up_ld, a->features, a->cols, b.up, b.k);
+  const Operand x = pack.operand(a->x, a->x_ld, a->rows, a->cols, b.x, b.k);
+  pack.launch(s);
   if (a->dx) {
-    const Operand gate = operand(a->dtype, a->gate, a->gate_ld, a->features, a->cols, ws, b.gate, b.k, s);
-    const Operand up_w = operand(a->dtype, a->up, a->up_ld, a->features, a->cols, ws, b.up, b.k, s);
     Product p = product_of(gate, a->cols, d, a->rows, 2 * half, es);
     p.r2 = up_w.p;
     p.k = (int)a->features;
@@ -256,7 +278,6 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
     }
   }
   if (a->dgate || a->dup) {
-    const Operand x = operand(a->dtype, a->x, a->x_ld, a->rows, a->cols, ws, b.x, b.k, s);
     Product p = product_of(x, a->cols, d, 2 * half, b.n, es);
     p.k = (int)a->rows;
     launch_product<T, StoreScaled, COLS_COLS, true>(
