@@ -102,16 +102,18 @@ __device__ __forceinline__ double block_sum(double v, int order, double* lds) {
   return v;
 }
 
-// The tensor of a tile: the last whose first tile is not past it.
-template <typename Tab>
-__device__ __forceinline__ int tensor_of(const Tab& t, uint32_t tile) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (t.first[mid] <= tile) lo = mid;
-    else hi = mid - 1;
+// The tensor of a tile: the last whose first tile is not past it.  Each lane compares
+// a few entries (those past the last tensor are past every tile): one trip to memory
+// instead of a binary search's eight.
+template <int N, bool OUT>
+__device__ __forceinline__ int tensor_of(const Table<N, OUT>& t, uint32_t tile) {
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < (N + 63) / 64; ++j) {
+    const int i = j * 64 + (int)(threadIdx.x & 63);
+    n += __popcll(__ballot(i < N && t.first[min(i, N - 1)] <= tile));
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 template <int ORDER>
@@ -150,7 +152,7 @@ __global__ __launch_bounds__(kBlock) void k_grad_norm_join(const double* sums, i
 }
 
 // Float32 goes four elements per lane and access, so that a wave's access is one
-// stretch of memory (a chunk of 8 is two accesses 32 bytes apart; QUADS_MEASURED).
+// stretch of memory (a chunk of 8 would be two accesses 32 bytes apart).
 template <typename O>
 __device__ __forceinline__ void clip_tile_f32(const void* grad, void* out, int64_t n, int64_t start, float c) {
   typedef uint32_t v2u __attribute__((ext_vector_type(2), aligned(2)));
@@ -341,6 +343,7 @@ void each_table(const fo_grad* list, int32_t count, int64_t total, Take&& take, 
   t.tiles = 0;
   auto flush = [&] {
     if (!t.count) return;
+    std::fill(t.first + t.count, t.first + N, UINT32_MAX);
     const int64_t share = (kGroups * t.tiles + total - 1) / total;
     launch(t, (unsigned)std::max<int64_t>(1, std::min<int64_t>(share, t.tiles)));
     t.count = 0;
