@@ -37,7 +37,14 @@ template <typename T, typename E, Form F, bool NARROW_OK>
 void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStream_t s) {
   p.tiles_r = c.tiles_r; p.tiles_c = c.tiles_c; p.slices = c.slices;
   if constexpr (NARROW_OK)
-    if (c.kind == NARROW) return launch_tile<T, E, F, 1, 1, 2, 1, 3>(p, e, s);
+    if (c.kind == NARROW) {
+      // three stages let four workgroups share a compute unit; where two do (512 tiles and
+      // fewer) a fourth stage is more under way: one token through two 14336 x 4096 bf16
+      // weights from memory 47.6 us against 49.5; six stages, or steps fetched in pairs,
+      // gave no more.  786 tiles (50257 x 768) take 25 us with four stages, 18 with three.
+      if ((int64_t)c.tiles_r * c.tiles_c * c.slices <= 2 * kUnits) return launch_tile<T, E, F, 1, 1, 2, 1, 4>(p, e, s);
+      return launch_tile<T, E, F, 1, 1, 2, 1, 3>(p, e, s);
+    }
   if (c.kind == WIDE) return launch_tile<T, E, F, 2, 4, 4, 2, 2>(p, e, s);
   if (c.kind == MIDDLE) return launch_tile<T, E, F, 2, 2, 2, 2, 2>(p, e, s);
   launch_tile<T, E, F, 1, 2, 2, 1, 4>(p, e, s);

@@ -162,18 +162,18 @@ struct ByRows {
     for (int s = 0; s < 4; ++s)
       at[s] = (uint32_t)(first * 32 + (lane & 31)) * kStepBytes + (uint32_t)(((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
   }
-  __device__ __forceinline__ void fetch(int step, uint32_t lds, int wave) const {
+  // load i of a step
+  struct Step { uint32_t k; };
+  __device__ __forceinline__ Step at_step(int step) const { return {(uint32_t)step * kStepBytes}; }
+  __device__ __forceinline__ void fetch(const Step& step, int i, uint32_t lds, int wave) const {
+    const int chunk = i * WAVES + wave;
+    v4u b = buf[0];
+    if constexpr (DUAL) {             // 4 loads of 8 rows make a fragment
 #pragma unroll
-    for (int i = 0; i < loads; ++i) {
-      const int chunk = i * WAVES + wave;
-      v4u b = buf[0];
-      if constexpr (DUAL) {           // 4 loads of 8 rows make a fragment
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          b[e] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(chunk / 4 & 1 ? buf[1][e] : buf[0][e]));
-      }
-      load_to_lds(b, off[i], (uint32_t)step * kStepBytes, lds + (uint32_t)chunk * 1024);
+      for (int e = 0; e < 4; ++e)
+        b[e] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(chunk / 4 & 1 ? buf[1][e] : buf[0][e]));
     }
+    load_to_lds(b, off[i], step.k, lds + (uint32_t)chunk * 1024);
   }
   __device__ __forceinline__ v4u read(const uint8_t* lds, int s, int f) const {
     return *(const v4u*)(lds + at[s] + f * 32 * kStepBytes);
@@ -218,16 +218,16 @@ struct ByColumns {
     const int slot = (i * WAVES + wave) * 64 + lane, kk = slot / pieces, p = place(kk, slot % pieces);
     return (uint32_t)min(kk, rows - 1) * (uint32_t)ld + (uint32_t)min(p, left - 1) * 16;
   }
-  __device__ __forceinline__ void fetch(int step, uint32_t lds, int wave) const {
+  struct Step { v4u buf; int rows; };
+  __device__ __forceinline__ Step at_step(int step) const {
     const bool second = base2 && step >= joint;
     const int k0 = min((second ? step - joint : step) * kStep<T>, k - 1), rows = k - k0;
-    const v4u b = buffer_of((second ? base2 : base) + (int64_t)k0 * ld,
-                            (uint32_t)(min(rows, kStep<T>) - 1) * (uint32_t)ld + (uint32_t)left * 16);
-#pragma unroll
-    for (int i = 0; i < loads; ++i) {
-      const uint32_t o = rows < kStep<T> ? offset(i, wave, rows) : off[i];
-      load_to_lds(b, o, 0, lds + (uint32_t)(i * WAVES + wave) * 1024);
-    }
+    return {buffer_of((second ? base2 : base) + (int64_t)k0 * ld,
+                      (uint32_t)(min(rows, kStep<T>) - 1) * (uint32_t)ld + (uint32_t)left * 16), rows};
+  }
+  __device__ __forceinline__ void fetch(const Step& step, int i, uint32_t lds, int wave) const {
+    const uint32_t o = step.rows < kStep<T> ? offset(i, wave, step.rows) : off[i];
+    load_to_lds(step.buf, o, 0, lds + (uint32_t)(i * WAVES + wave) * 1024);
   }
   __device__ __forceinline__ v4u read(const uint8_t* lds, int s, int f) const {
     const uint8_t* p = lds + at[f];
@@ -267,66 +267,76 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& place, u
   if constexpr (c_rows) C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStepBytes, wc * FC, lane, wave);
   else C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStep<T>, 0, wc * FC, lane, wave);
 
-  auto fetch = [&](int step, int stage) {
-    const uint32_t base = lds0 + (uint32_t)stage * TL::stage_bytes;
-    R.fetch(first + step, base, wave);
-    C.fetch(first + step, base + TL::R * kStepBytes, wave);
-  };
-
 #pragma unroll
   for (int i = 0; i < FR; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j) acc[i][j] = (v16f)(0.0f);
 
-  // Fragments are read one sub-step ahead of the matrix instructions that use them, and
-  // the first of a step before the last instructions of the step before: no wave waits
-  // for LDS with its matrix unit idle.  The scheduling barriers keep that order.
+  // The sub-steps' work is interleaved by hand: each matrix instruction is followed by one
+  // read of the next sub-step's fragments, and in a step's last sub-step by its share of
+  // the loads of stage k + NS, so that neither a burst of reads nor one of loads leaves
+  // the matrix unit idle.  The scheduling barriers keep that order.
   v4u fr[2][FR], fc[2][FC];
-  auto read = [&](int s, int stage) {
-    const uint8_t* buf = lds_raw + stage * TL::stage_bytes;
-#pragma unroll
-    for (int i = 0; i < FR; ++i) fr[s & 1][i] = R.read(buf, s, i);
-#pragma unroll
-    for (int j = 0; j < FC; ++j) fc[s & 1][j] = C.read(buf + TL::R * kStepBytes, s, j);
+  constexpr int M = FR * FC, READS = FR + FC, RL = decltype(R)::loads, LOADS = TL::loads;
+  auto read_one = [&](int n, int s, const uint8_t* buf) {       // R's first, C's, the rest of R's
+    if (n == 0) fr[s & 1][0] = R.read(buf, s, 0);
+    else if (n <= FC) fc[s & 1][n - 1] = C.read(buf + TL::R * kStepBytes, s, n - 1);
+    else fr[s & 1][n - FC] = R.read(buf, s, n - FC);
   };
-  auto use = [&](int s) {
+  // sub-step s; reads sub-step (s + 1) % 4 from `next`; then(m): after matrix instruction m
+  auto sub_step = [&](int s, const uint8_t* next, auto&& then) {
 #pragma unroll
-    for (int i = 0; i < FR; ++i)
+    for (int m = 0; m < M; ++m) {
+      acc[m / FC][m % FC] = mma<T>(fr[s & 1][m / FC], fc[s & 1][m % FC], acc[m / FC][m % FC]);
+      if (m < READS) read_one(m, (s + 1) & 3, next);
+      if (m == M - 1) {
 #pragma unroll
-      for (int j = 0; j < FC; ++j) acc[i][j] = mma<T>(fr[s & 1][i], fc[s & 1][j], acc[i][j]);
+        for (int n = M; n < READS; ++n) read_one(n, (s + 1) & 3, next);
+      }
+      then(m);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // loads [lo, hi) of a stage
+  auto fetch = [&](const auto& r, const auto& c, int stage, int lo, int hi) {
+    const uint32_t base = lds0 + (uint32_t)stage * TL::stage_bytes;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      if (i >= lo && i < hi) {
+        if (i < RL) R.fetch(r, i, base, wave);
+        else C.fetch(c, i - RL, base + TL::R * kStepBytes, wave);
+      }
   };
 
 #pragma unroll
   for (int s = 0; s < NS; ++s)
-    if (s < n) fetch(s, s);
+    if (s < n) fetch(R.at_step(first + s), C.at_step(first + s), s, 0, LOADS);
   if (n >= NS) wait_loads<(NS - 1) * TL::loads>();
   else wait_loads<0>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  read(0, 0);
+#pragma unroll
+  for (int i = 0; i < READS; ++i) read_one(i, 0, lds_raw);
   int stage = 0;
   for (int k = 0; k < n; ++k) {
     const int next = stage == NS - 1 ? 0 : stage + 1;
 #pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      read(s + 1, stage);
-      __builtin_amdgcn_sched_barrier(0);
-      use(s);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (k + 1 < n) {
-      // this wave has read all of stage k, and its loads of stage k + 1 have arrived
-      // when at most those of later stages are under way
-      if (NS > 2 && k + NS <= n) wait_loads<(NS - 2) * TL::loads>();
-      else wait_loads<0>();
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      // ... and so have the others: stage k's place takes stage k + NS
-      read(0, next);
-      __builtin_amdgcn_sched_barrier(0);
-      if (k + NS < n) fetch(k + NS, stage);
-    }
-    use(3);
+    for (int s = 0; s < 3; ++s) sub_step(s, lds_raw + stage * TL::stage_bytes, [](int) {});
+    // this wave has read all of stage k, and its loads of stage k + 1 have arrived when at
+    // most those of later stages are under way
+    if (NS > 2 && k + NS <= n) wait_loads<(NS - 2) * TL::loads>();
+    else wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // ... and so have the others: stage k's place takes stage k + NS.  (The last step
+    // reads what nothing uses: with matrix instructions on two paths their registers
+    // would be copied from one to the other, and do not fit.)
+    const bool more = k + NS < n;
+    const auto r = R.at_step(first + min(k + NS, n - 1));
+    const auto c = C.at_step(first + min(k + NS, n - 1));
+    sub_step(3, lds_raw + next * TL::stage_bytes, [&](int m) {
+      if (more) fetch(r, c, stage, m * LOADS / M, (m + 1) * LOADS / M);
+    });
     stage = next;
   }
 }
