@@ -183,12 +183,12 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
     const Operand w = pack.operand(static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es, a->weight_ld, nv,
                                    a->cols, b.w, b.k);
     pack.launch(s);
-    const Operand dz = {at(ws, b.dz), nvp};
+    const Operand dz = {at(ws, b.dz), nvp + kGap};
     const Product pz = product_of(w, nv, x, a->rows, b.k, es);
     // tokens in whole steps: the padding is written too (as zeros)
     launch_product<T, LogitGradients, ROWS_ROWS, false>(
         pz, cut(a->dtype, nv, b.n, pz.steps, false, false, false),
-        {at(ws, b.dz), nvp, a->lse, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
+        {at(ws, b.dz), dz.ld, a->lse, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
          (float)a->smoothing}, s);
     if (a->dx) {
       Product px = product_of(w, a->cols, dz, a->rows, nvp, es);
@@ -261,9 +261,9 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
   const int64_t es = elem_bytes<T>, half = b.half;
   void* ws = a->workspace;
   const GatedBwd g = {a->dy, a->dy_ld, a->g, a->u, at(ws, b.d), (int)a->rows, (int)b.n, (int)a->features, (int)half,
-                      a->activation};
+                      2 * half + kGap, a->activation};
   hipLaunchKernelGGL((k_gated_bwd<T>), grid_of((b.n * half / 8 + 255) / 256), 256, 0, s, g);
-  const Operand d = {at(ws, b.d), 2 * half};
+  const Operand d = {at(ws, b.d), g.ld};
   Packing pack = {a->dtype, ws};
   const Operand gate = pack.operand(a->gate, a->gate_ld, a->features, a->cols, b.gate, b.k);
   const Operand up_w = pack.operand(a->up, a->up_ld, a->features, a->cols, b.up, b.k);

@@ -72,7 +72,7 @@ static bool loss(const fo_loss& a) {
     }
     if (dx) CHECK(covers(b.dx, a.cols, a.rows, b.piece * es / 128, false));
     CHECK(apart({{b.unit, a.rows * 4}, {b.factor, 4}, {b.x, a.rows * b.k * es}, {b.w, std::min(b.piece, a.vocab) * b.k * es},
-                 {b.xm, b.n * b.k * es}, {b.dz, b.n * b.piece * es}, {b.sums, b.dx.slices * a.rows * b.sums_ld * 4}}, b.bytes));
+                 {b.xm, b.n * b.k * es}, {b.dz, b.n * (b.piece + kGap) * es}, {b.sums, b.dx.slices * a.rows * b.sums_ld * 4}}, b.bytes));
   }
   return true;
 }
@@ -89,7 +89,7 @@ static bool gated(const fo_gated& a) {
     CHECK(b.half % 64 == 0 && b.half >= a.features && 2 * b.half * es <= kMaxRowBytes);
     if (dx) CHECK(covers(b.dx, a.cols, a.rows, 2 * b.half * es / 128, false));
     if (dw) CHECK(covers(cut(a.dtype, a.cols, 2 * b.half, b.n * es / 128, false, true, false), a.cols, 2 * b.half, b.n * es / 128, false));
-    CHECK(apart({{b.d, b.n * 2 * b.half * es}, {b.x, a.rows * b.k * es}, {b.gate, a.features * b.k * es},
+    CHECK(apart({{b.d, b.n * (2 * b.half + kGap) * es}, {b.x, a.rows * b.k * es}, {b.gate, a.features * b.k * es},
                  {b.up, a.features * b.k * es}, {b.sums, b.dx.slices * a.rows * b.sums_ld * 4}}, b.bytes));
   }
   return true;
