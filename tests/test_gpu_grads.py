@@ -94,6 +94,31 @@ def test_clipping_in_place(sizes, p, dtype):
     assert all(torch.equal(a, b) for a, b in zip(gs, after))
 
 
+@pytest.mark.parametrize("dtype,out", [("f32", "bf16"), ("bf16", "f32"), ("fp16", "fp16")])
+def test_large_lists_into_other_tensors(dtype, out):
+    # past 4096 tiles (2^26 elements) a workgroup has half a tile; tensors that end in a
+    # first half, at its end and in a second, behind guards
+    sizes = [16384 * 4096, 3, 16384 + 8192, 16384 + 8193, 8191, 1, 2 * 16384 - 1]
+    gs = make(sizes, dtype, 4)
+    buffer = torch.full((sum(sizes) + 8 * len(sizes),), 7, dtype=TYPES[out], device="cuda")
+    outs, at = [], 0
+    for n in sizes:
+        outs.append(buffer[at:at + n])
+        at += n + 8
+    inside = make([1000], dtype, 5)[0]
+    before, want = inside.clone(), norm64(gs + [inside], 2)
+    norm = clip_grads(gs + [inside], 0.37, out=outs + [inside])[1]
+    check("norm", norm, want, 2 * U * want)
+    check_clipped("large", outs + [inside], gs + [before], factor64(want, 0.37))
+    again = clip_grads(gs, 1e9, out=outs)[1]            # the bound holds: a conversion
+    assert all(torch.equal(o, g.to(o.dtype)) for o, g in zip(outs, gs))
+    check("again", again, norm64(gs, 2), 2 * U * norm64(gs, 2))
+    at = 0
+    for n in sizes:
+        at += n + 8
+        assert (buffer[at - 8:at] == 7).all()
+
+
 def test_types_in_one_list():
     gs = [make([1000 + i], d, i)[0] for i, d in enumerate(list(TYPES) * 3)]
     before = [g.clone() for g in gs]
