@@ -67,8 +67,7 @@ struct Packing {
   Operand copy(const void* src, int64_t ld, int64_t rows, int64_t cols, int64_t offset, int64_t k, int64_t dst_rows,
                const int64_t* target = nullptr, int64_t ignore = 0) {
     const int64_t es = (int64_t)elem_size(dtype);
-    const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (rows == 1 || ld * es % 16 == 0);
-    jobs.job[n++] = {src, ld, at(workspace, offset), k, (int)rows, (int)cols, (int)dst_rows, wide, target, ignore};
+    jobs.job[n++] = {src, ld, at(workspace, offset), k, (int)rows, (int)cols, (int)dst_rows, target, ignore};
     most = std::max(most, dst_rows * k * es / 16);
     return {at(workspace, offset), k};
   }
