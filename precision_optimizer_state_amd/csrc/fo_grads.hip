@@ -116,6 +116,13 @@ __device__ __forceinline__ int tensor_of(const Table<N, OUT>& t, uint32_t tile) 
   return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
+// One read of everything, squares summed in 64 bits (a product of two floats is exact
+// there, and 2^40 terms lose nothing a float would show), in an order that the list alone
+// decides.  Bound by memory: 1.745e9 floats 1.11 ms (6.3 TB/s, of the 7.1 that a bare
+// read reaches), 124e6 bf16 38.7 us (6.4, partly from the memory-side cache), 25.6e6
+// fp16 12 us.  Consecutive tiles per workgroup: with tiles dealt out in turn every tile
+// needs its tensor looked up, 56 us instead of 40.  4096 workgroups gain nothing.
+// Float32 by four elements per lane and access, as clipping reads it, took 1.89 ms.
 template <int ORDER>
 __global__ __launch_bounds__(kBlock) void k_grad_norm(Plain t, double* sums) {
   __shared__ double lds[kBlock / 64];
@@ -259,7 +266,8 @@ struct ClipArgs { const double* sums; float* norm; double max_norm; int count, o
 
 // Every workgroup joins the partial sums for itself (8 KB from L2: a launch less, and
 // no workgroup waits for another).  Tiles go from the last to the first: what the norm
-// read last is still in the memory-side cache.
+// read last is still in the memory-side cache.  Where the bound holds it ends here: 4.5
+// us.  Scaling 2^30 bf16 elements in place takes 0.98 ms (4.4 TB/s).
 template <typename Tab, bool OUT>
 __global__ __launch_bounds__(kBlock) void k_grad_clip(Tab t, ClipArgs a) {
   __shared__ double lds[kBlock / 64];
