@@ -27,7 +27,7 @@
 // banks.  Floats are read one by one.
 //
 // What bounds it.  A step of a 256 x 256 tile of 16-bit elements is 256 matrix
-// instructions of 16 cycles on 4 units, 0.43 us at 2.4 GHz; 8192 x 4096 x 128256 takes
+// instructions of 32 cycles on 4 units, 0.85 us at 2.4 GHz; 8192 x 4096 x 128256 takes
 // 1.67 us per step and round, 1318 TFLOP/s of 2500 (libraries' products of such sizes
 // reach 1240 to 1430 on the same card).  The matrix units are busy 75 % of the cycles
 // there and the clock has come down to 1.67 GHz: power is what is left to save.  With
