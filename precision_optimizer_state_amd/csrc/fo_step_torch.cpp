@@ -8,6 +8,8 @@
 
 #include "fo_torch.hpp"
 
+#include <algorithm>
+
 namespace {
 
 // A workspace of the current stream's: at least one byte, so that it has an address.
@@ -334,6 +336,13 @@ Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>& outs, d
       if (!to.is_same(o)) back.emplace_back(o, to);
     }
     list[i] = {from.data_ptr(), to.data_ptr(), from.numel(), dtype_of(from), dtype_of(to)};
+  }
+  // (the library refuses a tensor that is listed twice; copies hide it)
+  std::sort(back.begin(), back.end(), [](const auto& a, const auto& b) { return a.first.data_ptr() < b.first.data_ptr(); });
+  for (size_t i = 1; i < back.size(); ++i) {
+    const Tensor &a = back[i - 1].first, &b = back[i].first;
+    TORCH_CHECK_VALUE(a.numel() == 0 || a.data_ptr() != b.data_ptr() || a.sizes() != b.sizes() || a.strides() != b.strides(),
+                      "a tensor is listed twice");
   }
   const Tensor norm = at::empty({}, on_current_device(at::kFloat));
   const Workspace ws = grad_workspace();

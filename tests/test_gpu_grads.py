@@ -259,6 +259,18 @@ def test_refusals():
         grad_norm([g, g.cpu()])
 
 
+def test_a_strided_tensor_listed_twice_is_refused():
+    # such tensors are clipped through copies, which would hide it
+    buffer = torch.randn(8, 10, device="cuda")
+    before = buffer.clone()
+    with pytest.raises(ValueError, match="listed twice"):
+        clip_grads([buffer[:, :3], buffer[:, 5:], buffer[:, :3]], 1.0)
+    assert torch.equal(buffer, before)
+    norm = clip_grads([buffer[:, :5], buffer[:, 5:]], 1.0)[1]      # its halves may be
+    check("norm", norm, norm64([before], 2), 2 * U * norm64([before], 2))
+    check_clipped("halves", [buffer], [before], factor64(norm64([before], 2), 1.0))
+
+
 def test_a_graph_that_saved_a_clipped_gradient_is_refused():
     g = torch.randn(10, device="cuda")
     a = torch.randn(10, device="cuda", requires_grad=True)
