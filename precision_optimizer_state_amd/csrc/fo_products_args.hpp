@@ -63,13 +63,13 @@ constexpr int64_t kUnits = 256;                                 // compute units
 // compute unit, of the others 512; a last round of half of that or less takes the second
 // figure of each pair.  16-bit types: 1.67 per step (wide), 0.94 and 0.59 (middle), 0.36
 // and 0.31 (small); float32, whose matrix instructions take 8 times as long, 7.4, 4 and
-// 2, and 1.1 (a small tile's two waves leave half of the matrix units idle).  What a
+// 2, 1.1 and 0.6.  What a
 // round takes besides its steps differs with the epilogue (4 to 15, 2 to 8 and 3 to 5):
 // its middle is taken.  (Since these were measured the main loop has become 3 to 5 %
 // faster, wide and middle tiles alike.)
 inline double round_time(TileKind k, bool f32, bool half, double steps) {
   const double fixed = k == WIDE ? 9.0 : k == MIDDLE ? 4.5 : 4.0;
-  const double step = f32 ? (k == WIDE ? 7.4 : k == MIDDLE ? (half ? 2.0 : 4.0) : 1.1)
+  const double step = f32 ? (k == WIDE ? 7.4 : k == MIDDLE ? (half ? 2.0 : 4.0) : (half ? 0.6 : 1.1))
                           : (k == WIDE ? 1.67 : k == MIDDLE ? (half ? 0.59 : 0.94) : (half ? 0.31 : 0.36));
   return fixed + step * steps;
 }

@@ -141,9 +141,11 @@ template <int N> __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
 }
 
-template <int WR, int WC, int FR, int FC, int NS>
+// KS: groups of waves that share a tile's sub-steps (each has its own sums of every
+// place of the tile, which are added at the end).
+template <int WR, int WC, int FR, int FC, int NS, int KS>
 struct Tile {
-  static constexpr int R = WR * FR * 32, C = WC * FC * 32, waves = WR * WC, threads = waves * 64;
+  static constexpr int R = WR * FR * 32, C = WC * FC * 32, group = WR * WC, groups = KS, waves = group * KS, threads = waves * 64;
   static constexpr int stage_bytes = (R + C) * kStepBytes, lds_bytes = stage_bytes * NS;
   static constexpr int loads = (R + C) / 8 / waves;            // of a wave, per stage
   static_assert((R + C) / 8 % waves == 0 && R / 8 % waves == 0, "loads are shared evenly");
@@ -158,8 +160,9 @@ struct ByRows {
   v4u buf[DUAL ? 2 : 1];
 
   // rows past the last are read as the last again (their sums are not used)
+  // `sub`: the sub-step that this wave calls its first
   __device__ __forceinline__ void init(const void* base, const void* base2, int64_t ld, int row0, int rows, int k_bytes,
-                                       int first, int lane, int wave) {
+                                       int first, int sub, int lane, int wave) {
     const int mine = DUAL ? N / 2 : N;
 #pragma unroll
     for (int i = 0; i < loads; ++i) {
@@ -173,7 +176,7 @@ struct ByRows {
     if constexpr (DUAL) buf[1] = buffer_of((const uint8_t*)base2 + (int64_t)row0 * ld, bytes);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      at[s] = (uint32_t)(first * 32 + (lane & 31)) * kStepBytes + (uint32_t)(((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
+      at[s] = (uint32_t)(first * 32 + (lane & 31)) * kStepBytes + (uint32_t)(((2 * ((s + sub) & 3) + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
   }
   // load i of a step
   struct Step { uint32_t k; };
@@ -208,7 +211,7 @@ struct ByColumns {
     return pieces >= 16 ? p ^ (k & 3) << 2 : pieces == 8 ? p ^ (k >> 1 & 1) << 2 : p;
   }
   __device__ __forceinline__ void init(const void* b, const void* b2, int64_t ld_, int row0, int rows, int k_, int joint_,
-                                       int first, int lane_, int wave) {
+                                       int first, int sub, int lane_, int wave) {
     base = (const uint8_t*)b + (int64_t)row0 * elem_bytes<T>;
     base2 = b2 ? (const uint8_t*)b2 + (int64_t)row0 * elem_bytes<T> : nullptr;
     ld = ld_; k = k_; joint = joint_; lane = lane_;
@@ -219,10 +222,10 @@ struct ByColumns {
     for (int f = 0; f < F; ++f) {
       if constexpr (is_f32<T>) {
         const int row = (first + f) * 32 + (lane & 31), kk = (lane >> 5) * 4;
-        at[f] = (uint32_t)(kk * row_bytes + place(kk, row / 4) * 16 + row % 4 * 4);
+        at[f] = (uint32_t)((sub * 8 + kk) * row_bytes + place(kk, row / 4) * 16 + row % 4 * 4);
       } else {
         const int i = lane & 15, kk = (lane >> 5) * 8 + i / 4, row = (first + f) * 32 + (lane >> 4 & 1) * 16 + i % 4 * 4;
-        at[f] = (uint32_t)(kk * row_bytes + place(kk, row / 8) * 16 + row % 8 * 2);
+        at[f] = (uint32_t)((sub * 16 + kk) * row_bytes + place(kk, row / 8) * 16 + row % 8 * 2);
       }
     }
   }
@@ -268,17 +271,19 @@ template <typename T, typename TL, int WR, int WC, int FR, int FC, int NS, Form 
 __device__ __forceinline__ void multiply(const Product& p, const Place& place, uint8_t* lds_raw, v16f (&acc)[FR][FC]) {
   constexpr bool dual = FORM == DUAL_ROWS, r_rows = FORM == ROWS_ROWS || dual, c_rows = FORM != COLS_COLS;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave % WR, wc = wave / WR;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave % WR, wc = wave % TL::group / WR;
+  constexpr int SUBS = 4 / TL::groups;                          // of a wave
+  const int sub = wave / TL::group * SUBS;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds_raw;
   const int first = (int)((int64_t)place.slice * p.steps / p.slices);
   const int n = (int)((int64_t)(place.slice + 1) * p.steps / p.slices) - first;
 
   typename Pick<r_rows, ByRows<T, TL::R, FR, TL::waves, dual>, ByColumns<T, TL::R, FR, TL::waves>>::type R;
   typename Pick<c_rows, ByRows<T, TL::C, FC, TL::waves, false>, ByColumns<T, TL::C, FC, TL::waves>>::type C;
-  if constexpr (r_rows) R.init(p.r, p.r2, p.r_ld, place.r * (dual ? TL::R / 2 : TL::R), p.nr, p.steps * kStepBytes, wr * FR, lane, wave);
-  else R.init(p.r, p.r2, p.r_ld, place.r * TL::R, p.nr, p.k, p.joint, wr * FR, lane, wave);
-  if constexpr (c_rows) C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStepBytes, wc * FC, lane, wave);
-  else C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStep<T>, 0, wc * FC, lane, wave);
+  if constexpr (r_rows) R.init(p.r, p.r2, p.r_ld, place.r * (dual ? TL::R / 2 : TL::R), p.nr, p.steps * kStepBytes, wr * FR, sub, lane, wave);
+  else R.init(p.r, p.r2, p.r_ld, place.r * TL::R, p.nr, p.k, p.joint, wr * FR, sub, lane, wave);
+  if constexpr (c_rows) C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStepBytes, wc * FC, sub, lane, wave);
+  else C.init(p.c, nullptr, p.c_ld, place.c * TL::C, p.nc, p.steps * kStep<T>, 0, wc * FC, sub, lane, wave);
 
 #pragma unroll
   for (int i = 0; i < FR; ++i)
@@ -296,15 +301,15 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& place, u
     else if (n <= FC) fc[s & 1][n - 1] = C.read(buf + TL::R * kStepBytes, s, n - 1);
     else fr[s & 1][n - FC] = R.read(buf, s, n - FC);
   };
-  // sub-step s; reads sub-step (s + 1) % 4 from `next`; then(m): after matrix instruction m
+  // sub-step s; reads sub-step s + 1 (or the first) from `next`; then(m): after matrix instruction m
   auto sub_step = [&](int s, const uint8_t* next, auto&& then) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       acc[m / FC][m % FC] = mma<T>(fr[s & 1][m / FC], fc[s & 1][m % FC], acc[m / FC][m % FC]);
-      if (m < READS) read_one(m, (s + 1) & 3, next);
+      if (m < READS) read_one(m, (s + 1) % SUBS, next);
       if (m == M - 1) {
 #pragma unroll
-        for (int n = M; n < READS; ++n) read_one(n, (s + 1) & 3, next);
+        for (int n = M; n < READS; ++n) read_one(n, (s + 1) % SUBS, next);
       }
       then(m);
       __builtin_amdgcn_sched_barrier(0);
@@ -334,7 +339,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& place, u
   for (int k = 0; k < n; ++k) {
     const int next = stage == NS - 1 ? 0 : stage + 1;
 #pragma unroll
-    for (int s = 0; s < 3; ++s) sub_step(s, lds_raw + stage * TL::stage_bytes, [](int) {});
+    for (int s = 0; s < SUBS - 1; ++s) sub_step(s, lds_raw + stage * TL::stage_bytes, [](int) {});
     // this wave has read all of stage k, and its loads of stage k + 1 have arrived when at
     // most those of later stages are under way
     if (NS > 2 && k + NS <= n) wait_loads<(NS - 2) * TL::loads>();
@@ -347,10 +352,29 @@ __device__ __forceinline__ void multiply(const Product& p, const Place& place, u
     const bool more = k + NS < n;
     const auto r = R.at_step(first + min(k + NS, n - 1));
     const auto c = C.at_step(first + min(k + NS, n - 1));
-    sub_step(3, lds_raw + next * TL::stage_bytes, [&](int m) {
+    sub_step(SUBS - 1, lds_raw + next * TL::stage_bytes, [&](int m) {
       if (more) fetch(r, c, stage, m * LOADS / M, (m + 1) * LOADS / M);
     });
     stage = next;
+  }
+  if constexpr (TL::groups == 2) {
+    static_assert(TL::group * FR * FC * 4096 <= TL::lds_bytes, "sums of a group");
+    uint8_t* mine = lds_raw + ((wave % TL::group) * FR * FC * 4 * 64 + lane) * 16;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < FR * FC * 4; ++n) {
+      const v16f& a = acc[n / 4 / FC][n / 4 % FC];
+      if (sub) *(v4f*)(mine + n * 1024) = (v4f){a[n % 4 * 4], a[n % 4 * 4 + 1], a[n % 4 * 4 + 2], a[n % 4 * 4 + 3]};
+    }
+    __syncthreads();
+    if (!sub) {
+#pragma unroll
+      for (int n = 0; n < FR * FC * 4; ++n) {
+        const v4f b = *(const v4f*)(mine + n * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n / 4 / FC][n / 4 % FC][n % 4 * 4 + e] += b[e];
+      }
+    }
   }
 }
 
