@@ -6,6 +6,7 @@
 //
 // A workgroup of WR x WC waves owns a tile of WR*FR*32 rows of R by WC*FC*32 rows of C
 // and walks along k in steps of 128 bytes (64 elements of a 16-bit type, 32 floats).
+// (Small tiles have two such groups of waves, which share each step's four sub-steps.)
 // Operands go from memory straight into LDS, 16 bytes ("a piece") per lane, in a ring
 // of NS stages.
 //

@@ -6,7 +6,7 @@ import torch
 
 from precision_optimizer_state_amd import binding as B
 from precision_optimizer_state_amd import nn
-from step_helpers import TYPES, Gated, check, generator, normal
+from step_helpers import TYPES, U, Gated, check, generator, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -96,6 +96,19 @@ def test_layouts():
     against("one matrix", x, both[0], both[1], dy)
     both = torch.stack([gate, up], 1)
     against("alternating rows", x, both[:, 0], both[:, 1], dy)
+
+
+@pytest.mark.parametrize("rows", [1, 100, 300])
+def test_long_float32_sums_are_kept_in_two_levels(rows):
+    # 512 terms at a time, then 16 sums of those: of positive terms each product is off by
+    # at most 2 U (512 + 16 + 4) of itself (2 U per addition, should the instruction
+    # truncate), where one chain could be off by 2 U 8192.  y = g u for g far above 0,
+    # where gelu is the identity; 20 U for the activation and the last products.
+    gen = generator(16)
+    x, gate, up = (0.5 + 0.5 * torch.rand(n, 8192, generator=gen, device="cuda") for n in (rows, 70, 70))
+    y = nn.gated_linear(x, gate, up, "gelu").double()
+    want = (x.double() @ gate.double().t()) * (x.double() @ up.double().t())
+    check("y", y, want, (2 * 2 * (512 + 16 + 4) + 20) * U * want)
 
 
 def test_one_weight_for_both():
