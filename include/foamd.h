@@ -569,7 +569,7 @@ int fo_loss_forward_workspace(const fo_loss* args, int64_t* bytes);
  *   (whose x may hold anything, NaN included)
  *   dx = dz weight;  dweight = dz^T x
  * The logits are computed again, a piece of the vocabulary at a time; a piece's
- * dz, over the largest |f|, is rounded to dtype (half precision holds it times
+ * dz, over the largest finite |f|, is rounded to dtype (half precision holds it times
  * 2^15, so it resolves 2^-39).  Rows with an invalid target give NaN, in their
  * own dx and in dweight.
  */
