@@ -537,7 +537,7 @@ typedef struct fo_loss {
   const void*    weight;    /* vocab x cols */
   const int64_t* target;    /* rows; in [0, vocab) or ignore_index */
   float*         loss;      /* forward: rows, or 1 with a reduction (written) */
-  float*         lse;       /* rows: written by forward, read by backward */
+  float*         lse;       /* rows: written by forward, read by backward (see also `rest` below) */
   float*         count;     /* 1: the number of counted rows; written by forward with a reduction, read by backward for the mean */
   const float*   dloss;     /* backward: the loss's gradient, rows or 1 */
   void*          dx;        /* backward: rows x cols (written), or NULL */
@@ -563,7 +563,17 @@ int fo_loss_forward(const fo_loss* args, void* stream);
 int fo_loss_forward_workspace(const fo_loss* args, int64_t* bytes);
 
 /*
+ * fo_loss_forward_rest
+ * The same, with what lse's rounding to float32 left: rest[i] = log sum_v exp z_v -
+ * lse[i] (rows, written).  fo_loss_backward_rest reads it; fo_loss_backward, without
+ * it, makes the statistics of the logits again to find it, the same bits for one more
+ * product.  The workspaces are those of fo_loss_forward and fo_loss_backward.
+ */
+int fo_loss_forward_rest(const fo_loss* args, float* rest, void* stream);
+
+/*
  * fo_loss_backward
+ *   softmax(z) = exp((z - lse) - rest)
  *   dz = (softmax(z) - (1 - smoothing) [v = target] - smoothing / vocab) f
  *   with f the row's dloss (mean: over the count), 0 for rows not counted
  *   (whose x may hold anything, NaN included)
@@ -574,6 +584,7 @@ int fo_loss_forward_workspace(const fo_loss* args, int64_t* bytes);
  * own dx and in dweight.
  */
 int fo_loss_backward(const fo_loss* args, void* stream);
+int fo_loss_backward_rest(const fo_loss* args, const float* rest, void* stream);
 int fo_loss_backward_workspace(const fo_loss* args, int64_t* bytes);
 
 enum fo_activation { FO_SILU = 0, FO_GELU = 1, FO_GELU_TANH = 2 };

@@ -29,8 +29,8 @@ _STEP_EXPORTS = (
 )
 _ROW_EXPORTS = ("fo_dropout", "fo_norm_forward", "fo_norm_backward", "fo_norm_backward_workspace")
 _GRAD_EXPORTS = ("fo_grad_workspace", "fo_grad_norm", "fo_grad_clip")
-_PRODUCT_EXPORTS = ("fo_loss_forward", "fo_loss_forward_workspace", "fo_loss_backward", "fo_loss_backward_workspace",
-                    "fo_gated_forward", "fo_gated_forward_workspace", "fo_gated_backward", "fo_gated_backward_workspace")
+_PRODUCT_EXPORTS = ("fo_loss_forward", "fo_loss_forward_rest", "fo_loss_forward_workspace", "fo_loss_backward",
+                    "fo_loss_backward_rest", "fo_loss_backward_workspace", "fo_gated_forward", "fo_gated_forward_workspace", "fo_gated_backward", "fo_gated_backward_workspace")
 EXPORTS = _STEP_EXPORTS + _ROW_EXPORTS + _GRAD_EXPORTS + _PRODUCT_EXPORTS
 
 WFMT = {"bf16": FO_BF16, "fp16": FO_FP16}
@@ -163,6 +163,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             for way in ("forward", "backward"):
                 getattr(lib, f"fo_{name}_{way}").argtypes = [ctypes.POINTER(args), P]
                 getattr(lib, f"fo_{name}_{way}_workspace").argtypes = [ctypes.POINTER(args), ctypes.POINTER(c_int64)]
+        for way in ("forward", "backward"):
+            getattr(lib, f"fo_loss_{way}_rest").argtypes = [ctypes.POINTER(Loss), P, P]
         for name in _GRAD_EXPORTS + _PRODUCT_EXPORTS:
             getattr(lib, name).restype = c_int
     _lib = lib
@@ -179,7 +181,7 @@ def _load_rows() -> ctypes.CDLL:
 def _load_step() -> ctypes.CDLL:
     """The library with clipping, the loss and the gated block."""
     lib = load()
-    if not hasattr(lib, "fo_grad_clip") or not hasattr(lib, "fo_gated_backward"):
+    if not all(hasattr(lib, name) for name in _GRAD_EXPORTS + _PRODUCT_EXPORTS):
         raise ImportError(f"{LIB_PATH} has no gradient clipping, linear cross entropy or gated block: rebuild it with "
                           "__graft_entry__.build()")
     return lib
@@ -524,12 +526,15 @@ def fo_grad_clip(grads, outs, max_norm, norm_out, order=FO_NORM_2, workspace=Non
                                      _vec("norm_out", norm_out.view(-1), 1, torch.float32), ws, nbytes, _stream(stream)))
 
 
-def _run(name, args, workspace, stream, device) -> None:
+def _run(name, args, workspace, stream, device, rest=None) -> None:
     lib = _load_step()
     need = c_int64(0)
     _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
     held, args.workspace, args.workspace_bytes = _scratch(need.value, workspace, stream, device)
-    _check(getattr(lib, name)(ctypes.byref(args), _stream(stream)))
+    if rest is None:
+        _check(getattr(lib, name)(ctypes.byref(args), _stream(stream)))
+    else:
+        _check(getattr(lib, name + "_rest")(ctypes.byref(args), rest, _stream(stream)))
 
 
 def _loss_args(x, weight, target, reduction, ignore_index, smoothing):
@@ -544,28 +549,29 @@ def _loss_args(x, weight, target, reduction, ignore_index, smoothing):
 
 
 def fo_loss_forward(x, weight, target, loss_out, lse_out, count_out=None, reduction="mean", ignore_index=-100, smoothing=0.0,
-                    workspace=None, stream=None) -> None:
+                    workspace=None, stream=None, rest_out=None) -> None:
     """Softmax cross entropy of the logits x weight^T against target (int64).
-    loss_out: (rows,) or, with a reduction, (1,) float32; lse_out: (rows,);
-    count_out: (1,), with a reduction."""
+    loss_out: (rows,) or, with a reduction, (1,) float32; lse_out: (rows,), and
+    rest_out, what its rounding left; count_out: (1,), with a reduction."""
     import torch
     a = _loss_args(x, weight, target, reduction, ignore_index, smoothing)
     a.loss = _vec("loss_out", loss_out, x.shape[0] if a.reduction == 0 else 1, torch.float32)
     a.lse = _vec("lse_out", lse_out, x.shape[0], torch.float32)
     a.count = _vec("count_out", count_out, 1, torch.float32)
-    _run("fo_loss_forward", a, workspace, stream, x.device)
+    _run("fo_loss_forward", a, workspace, stream, x.device, _vec("rest_out", rest_out, x.shape[0], torch.float32))
 
 
 def fo_loss_backward(x, weight, target, lse, dloss, count=None, dx_out=None, dweight_out=None, reduction="mean",
-                     ignore_index=-100, smoothing=0.0, workspace=None, stream=None) -> None:
-    """The gradients of fo_loss_forward; dloss: (rows,) or (1,) float32."""
+                     ignore_index=-100, smoothing=0.0, workspace=None, stream=None, rest=None) -> None:
+    """The gradients of fo_loss_forward; dloss: (rows,) or (1,) float32.  Without `rest`,
+    the forward call's rest_out, the logits' statistics are computed again."""
     import torch
     a = _loss_args(x, weight, target, reduction, ignore_index, smoothing)
     a.lse, a.count = _vec("lse", lse, x.shape[0], torch.float32), _vec("count", count, 1, torch.float32)
     a.dloss, a.dloss_ld = _vec("dloss", dloss, x.shape[0] if a.reduction == 0 else 1, torch.float32), 1
     a.dx = _rows_out("dx_out", dx_out, x.shape, x.dtype)
     a.dweight = _rows_out("dweight_out", dweight_out, weight.shape, x.dtype)
-    _run("fo_loss_backward", a, workspace, stream, x.device)
+    _run("fo_loss_backward", a, workspace, stream, x.device, _vec("rest", rest, x.shape[0], torch.float32))
 
 
 def _gated_args(x, gate, up, activation):

@@ -135,8 +135,14 @@ int workspace_check(void* workspace, int64_t have, int64_t need, Arrays& ar) {
   return ar.add(workspace, "workspace", true, true, 1, need, 0, 1, 256);
 }
 
+void join_rows(LossRows r, hipStream_t s) {
+  r.width = 1;
+  while (r.width < 16 && r.width * 256 < r.rows) r.width *= 2;
+  hipLaunchKernelGGL(k_loss_rows, (unsigned)((r.rows + r.width - 1) / r.width), 1024, 0, s, r);
+}
+
 template <typename T>
-int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
+int run_loss_forward(const fo_loss* a, float* rest, const LossForward& f, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
   Packing pack = {a->dtype, a->workspace};
   const Operand x = pack.operand(a->x, a->x_ld, a->rows, a->cols, f.x, f.k);
@@ -149,19 +155,39 @@ int run_loss_forward(const fo_loss* a, const LossForward& f, hipStream_t s) {
   float* each = reduced ? (float*)at(a->workspace, f.each) : a->loss;
   const Product p = product_of(w, a->vocab, x, a->rows, f.k, es);
   launch_product<T, Statistics, ROWS_ROWS, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
-  int width = 1;
-  while (width < 16 && width * 256 < a->rows) width *= 2;
-  const LossRows r = {part, sums, chosen, a->target, each, a->lse, a->ignore_index, (int)a->rows, waves_r(f.c.kind) * f.c.tiles_r,
-                      (int)a->vocab, width, (float)a->smoothing};
-  hipLaunchKernelGGL(k_loss_rows, (unsigned)((a->rows + width - 1) / width), 1024, 0, s, r);
+  join_rows({part, sums, chosen, a->target, each, a->lse, nullptr, rest, a->ignore_index, (int)a->rows,
+             waves_r(f.c.kind) * f.c.tiles_r, (int)a->vocab, 1, (float)a->smoothing}, s);
   if (reduced)
     hipLaunchKernelGGL(k_loss_sum, 1, 1024, 0, s, (const float*)each, a->target, a->ignore_index, (int)a->rows,
                        (int)(a->reduction == FO_LOSS_MEAN), a->loss, a->count);
   return launch_check("loss forward launch");
 }
 
+// What lse's rounding left, from the forward pass's statistics made again: the same tiles
+// of the same sums (pieces are whole tiles), so the same bits.
 template <typename T>
-int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
+const float* find_rest(const fo_loss* a, const LossBackward& b, const Operand& x, Packing& pack, hipStream_t s) {
+  const int64_t es = elem_bytes<T>;
+  v2f* part = (v2f*)at(a->workspace, b.part);
+  float* rest = (float*)at(a->workspace, b.rest);
+  for (int64_t first = 0; first < a->vocab; first += b.piece) {
+    const int64_t nv = std::min(b.piece, a->vocab - first), tile = tile_r(b.statistics.kind);
+    const Operand w = pack.operand(static_cast<const uint8_t*>(a->weight) + first * a->weight_ld * es, a->weight_ld, nv,
+                                   a->cols, b.w, b.k);
+    pack.launch(s);
+    Cut c = b.statistics;
+    c.tiles_r = (int)((nv + tile - 1) / tile);
+    launch_product<T, Statistics, ROWS_ROWS, true>(
+        product_of(w, nv, x, a->rows, b.k, es), c,
+        {part + first / tile * waves_r(c.kind) * a->rows, nullptr, nullptr, a->target, a->ignore_index}, s);
+  }
+  join_rows({part, nullptr, nullptr, a->target, nullptr, nullptr, a->lse, rest, a->ignore_index, (int)a->rows, (int)b.parts,
+             (int)a->vocab, 1, 0.0f}, s);
+  return rest;
+}
+
+template <typename T>
+int run_loss_backward(const fo_loss* a, const float* rest, const LossBackward& b, hipStream_t s) {
   const int64_t es = elem_bytes<T>;
   void* ws = a->workspace;
   // a token's gradient is a common factor times its unit: 1 with a reduction
@@ -177,6 +203,7 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
   // dweight reads x without the tokens that are not counted: 0 times what they hold need not be 0
   Operand xm = {};
   if (a->dweight) xm = pack.copy(a->x, a->x_ld, a->rows, a->cols, b.xm, b.k, b.n, a->target, a->ignore_index);
+  if (!rest) rest = find_rest<T>(a, b, x, pack, s);
   // half precision holds gradients of logits times 2^15
   const float scale = __is_same(T, Fp16) ? 32768.0f : 1.0f;
   const int64_t slice = a->rows * b.sums_ld;
@@ -190,7 +217,7 @@ int run_loss_backward(const fo_loss* a, const LossBackward& b, hipStream_t s) {
     // tokens in whole steps: the padding is written too (as zeros)
     launch_product<T, LogitGradients, ROWS_ROWS, false>(
         pz, cut(a->dtype, nv, b.n, pz.steps, false, false, false),
-        {at(ws, b.dz), dz.ld, a->lse, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
+        {at(ws, b.dz), dz.ld, a->lse, rest, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
          (float)a->smoothing}, s);
     if (a->dx) {
       Product px = product_of(w, a->cols, dz, a->rows, nvp, es);
@@ -308,7 +335,7 @@ int fo_loss_forward_workspace(const fo_loss* a, int64_t* bytes) {
   return FO_OK;
 }
 
-int fo_loss_forward(const fo_loss* a, void* stream) {
+static int loss_forward_call(const fo_loss* a, float* rest, bool wanted, void* stream) {
   clear_error();
   FO_TRY(loss_checks(a));
   const bool any = a->rows > 0, reduced = a->reduction != FO_LOSS_NONE;
@@ -316,6 +343,7 @@ int fo_loss_forward(const fo_loss* a, void* stream) {
   FO_TRY(loss_inputs(a, ar));
   FO_TRY(ar.add(a->loss, "loss", true, any || reduced, reduced ? 1 : a->rows, 1, 1, 4));
   FO_TRY(ar.add(a->lse, "lse", true, any, a->rows, 1, 1, 4));
+  FO_TRY(ar.add(rest, "rest", true, wanted && any, a->rows, 1, 1, 4));
   FO_TRY(ar.add(a->count, "count", true, reduced, 1, 1, 1, 4));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!any) {
@@ -328,10 +356,12 @@ int fo_loss_forward(const fo_loss* a, void* stream) {
   const LossForward f = loss_forward(a);
   FO_TRY(workspace_check(a->workspace, a->workspace_bytes, f.bytes, ar));
   FO_TRY(ar.disjoint());
-  if (a->dtype == FO_BF16) return run_loss_forward<Bf16>(a, f, s);
-  if (a->dtype == FO_FP16) return run_loss_forward<Fp16>(a, f, s);
-  return run_loss_forward<F32>(a, f, s);
+  if (a->dtype == FO_BF16) return run_loss_forward<Bf16>(a, rest, f, s);
+  if (a->dtype == FO_FP16) return run_loss_forward<Fp16>(a, rest, f, s);
+  return run_loss_forward<F32>(a, rest, f, s);
 }
+int fo_loss_forward(const fo_loss* a, void* stream) { return loss_forward_call(a, nullptr, false, stream); }
+int fo_loss_forward_rest(const fo_loss* a, float* rest, void* stream) { return loss_forward_call(a, rest, true, stream); }
 
 int fo_loss_backward_workspace(const fo_loss* a, int64_t* bytes) {
   clear_error();
@@ -341,7 +371,7 @@ int fo_loss_backward_workspace(const fo_loss* a, int64_t* bytes) {
   return FO_OK;
 }
 
-int fo_loss_backward(const fo_loss* a, void* stream) {
+static int loss_backward_call(const fo_loss* a, const float* rest, bool given, void* stream) {
   clear_error();
   FO_TRY(loss_checks(a));
   const size_t es = elem_size(a->dtype);
@@ -349,6 +379,7 @@ int fo_loss_backward(const fo_loss* a, void* stream) {
   Arrays ar;
   FO_TRY(loss_inputs(a, ar));
   FO_TRY(ar.add(a->lse, "lse", false, any, a->rows, 1, 1, 4));
+  FO_TRY(ar.add(rest, "rest", false, given && any, a->rows, 1, 1, 4));
   FO_TRY(ar.add(a->count, "count", false, a->reduction == FO_LOSS_MEAN && any, 1, 1, 1, 4));
   FO_TRY(ar.add(a->dloss, "dloss", false, any, none ? a->rows : 1, 1, none ? a->dloss_ld : 1, 4));
   FO_TRY(ar.add(a->dx, "dx", true, false, a->rows, a->cols, a->cols, es));
@@ -364,10 +395,12 @@ int fo_loss_backward(const fo_loss* a, void* stream) {
   const LossBackward b = loss_backward(a, a->dx, a->dweight);
   FO_TRY(workspace_check(a->workspace, a->workspace_bytes, b.bytes, ar));
   FO_TRY(ar.disjoint());
-  if (a->dtype == FO_BF16) return run_loss_backward<Bf16>(a, b, s);
-  if (a->dtype == FO_FP16) return run_loss_backward<Fp16>(a, b, s);
-  return run_loss_backward<F32>(a, b, s);
+  if (a->dtype == FO_BF16) return run_loss_backward<Bf16>(a, rest, b, s);
+  if (a->dtype == FO_FP16) return run_loss_backward<Fp16>(a, rest, b, s);
+  return run_loss_backward<F32>(a, rest, b, s);
 }
+int fo_loss_backward(const fo_loss* a, void* stream) { return loss_backward_call(a, nullptr, false, stream); }
+int fo_loss_backward_rest(const fo_loss* a, const float* rest, void* stream) { return loss_backward_call(a, rest, true, stream); }
 
 int fo_gated_forward_workspace(const fo_gated* a, int64_t* bytes) {
   clear_error();

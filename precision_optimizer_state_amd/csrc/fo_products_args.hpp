@@ -128,7 +128,7 @@ inline double cut_time(int dtype, const Cut& c, int64_t steps) {
 // most about 2^28 elements (512 MB in 16 bits).  Of the sizes down to half of that the
 // one whose three products fill the card's last rounds best (8192 tokens, 768 columns,
 // 50257 places: 21504 instead of 25344, whose weight gradients are 297 wide tiles on 256
-// compute units).
+// compute units).  Where there are several they are multiples of 256: whole tiles of any kind.
 constexpr int64_t kPieceElems = int64_t(1) << 28;
 inline int64_t piece_vocab(int dtype, int64_t tokens, int64_t cols, int64_t vocab) {
   const int64_t es = (int64_t)elem_size(dtype), n = padded(tokens);
@@ -176,7 +176,10 @@ inline LossForward loss_forward(const fo_loss* a) {
 }
 
 struct LossBackward {
-  int64_t unit = -1, factor = -1, x = -1, w = -1, xm = -1, dz = -1, sums = -1, bytes = 0;
+  int64_t unit = -1, factor = -1, rest = -1, x = -1, w = -1, xm = -1, dz = -1, sums = -1, bytes = 0;
+  // without the forward pass's `rest`: its statistics again, where dz comes later
+  int64_t part = -1, parts = 0;
+  Cut statistics = {};
   int64_t k, n, piece, sums_ld;                                 // columns and tokens in whole steps; vocabulary per piece
   Cut dx = {};                                                  // of a whole piece
 };
@@ -194,7 +197,10 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   if (!direct(a->x, a->rows, a->cols, a->x_ld, a->dtype)) b.x = l.take(a->rows * b.k * es);
   if (!direct(a->weight, a->vocab, a->cols, a->weight_ld, a->dtype)) b.w = l.take(std::min(b.piece, a->vocab) * b.k * es);
   if (dw) b.xm = l.take(b.n * b.k * es);
-  b.dz = l.take(b.n * (b.piece + kGap) * es);
+  b.rest = l.take(a->rows * 4);
+  b.statistics = cut(a->dtype, a->vocab, a->rows, b.k * es / 128, false, true, false);
+  b.parts = (int64_t)waves_r(b.statistics.kind) * b.statistics.tiles_r;
+  b.part = b.dz = l.take(std::max(b.n * (b.piece + kGap) * es, b.parts * a->rows * 8));
   b.sums_ld = up(a->cols, 4);
   if (dx) {
     b.dx = cut(a->dtype, a->cols, a->rows, b.piece * es / 128, false, true, true);

@@ -85,15 +85,17 @@ struct LossArgs {
   }
 };
 
+// `lse`: a row of log sums of exponentials and, where a backward pass will want them, one
+// of what their rounding left
 struct LossOut { Tensor loss, lse, count; };
 
 LossOut loss_forward(const Tensor& x, const Tensor& weight, const Tensor& target, int64_t ignore_index, int32_t reduction,
-                     double smoothing) {
+                     double smoothing, bool keep) {
   LossArgs l(x, weight, target, ignore_index, reduction, smoothing);
   const auto f32 = x.options().dtype(at::kFloat);
   LossOut o;
   o.loss = reduction == FO_LOSS_NONE ? at::empty(target.sizes(), f32) : at::empty({}, f32);
-  o.lse = at::empty({l.a.rows}, f32);
+  o.lse = at::empty({keep ? 2 : 1, l.a.rows}, f32);
   if (reduction != FO_LOSS_NONE) o.count = at::empty({}, f32);
   l.a.loss = static_cast<float*>(o.loss.data_ptr());
   l.a.lse = static_cast<float*>(o.lse.data_ptr());
@@ -103,14 +105,14 @@ LossOut loss_forward(const Tensor& x, const Tensor& weight, const Tensor& target
   const Workspace ws(bytes, x.options());
   l.a.workspace = ws.ptr();
   l.a.workspace_bytes = ws.bytes;
-  check(fo_loss_forward(&l.a, current_stream()));
+  check(keep ? fo_loss_forward_rest(&l.a, l.a.lse + l.a.rows, current_stream()) : fo_loss_forward(&l.a, current_stream()));
   return o;
 }
 
 struct Loss : torch::autograd::Function<Loss> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const Tensor& target,
                         int64_t ignore_index, int64_t reduction, double smoothing) {
-    LossOut o = loss_forward(x, weight, target, ignore_index, static_cast<int32_t>(reduction), smoothing);
+    LossOut o = loss_forward(x, weight, target, ignore_index, static_cast<int32_t>(reduction), smoothing, true);
     ctx->save_for_backward({x, weight, target, o.lse, o.count});
     put(ctx, ignore_index, smoothing, static_cast<int32_t>(reduction));
     ctx->set_materialize_grads(false);
@@ -139,7 +141,7 @@ struct Loss : torch::autograd::Function<Loss> {
     const Workspace ws(bytes, x.options());
     l.a.workspace = ws.ptr();
     l.a.workspace_bytes = ws.bytes;
-    check(fo_loss_backward(&l.a, current_stream()));
+    check(fo_loss_backward_rest(&l.a, l.a.lse + l.a.rows, current_stream()));
     return once(std::move(out));
   }
 };
@@ -157,7 +159,7 @@ Tensor linear_cross_entropy(const Tensor& x, const Tensor& weight, const Tensor&
     check_capture({&x, &weight});
     return Loss::apply(x, weight, target, ignore_index, reduction, smoothing);
   }
-  return loss_forward(x, weight, target, ignore_index, static_cast<int32_t>(reduction), smoothing).loss;
+  return loss_forward(x, weight, target, ignore_index, static_cast<int32_t>(reduction), smoothing, false).loss;
 }
 
 // ---------------------------------------------------------------------------
