@@ -1,5 +1,6 @@
 // More of the products' host half (csrc/fo_products_args.hpp) against brute force: where
-// the backward pass of the loss keeps the statistics that it makes again.
+// the backward pass of the loss keeps the statistics that it makes again, and float32
+// sums of long k.
 #include <cstdarg>
 #include <cstdio>
 #include <random>
@@ -44,6 +45,15 @@ static bool loss(const fo_loss& a) {
   return true;
 }
 
+// Wide tiles' float32 sums are one chain each: of at most 64 steps, 2048 terms.
+static bool chains(int64_t nr, int64_t nc, int64_t steps) {
+  for (int form = 0; form < 8; ++form) {
+    const Cut c = cut(FO_F32, nr, nc, steps, form & 1, form & 2, form & 4);
+    CHECK(c.slices >= 1 && (c.kind != WIDE || (steps + c.slices - 1) / c.slices <= 64));
+  }
+  return true;
+}
+
 int main() {
   std::mt19937_64 rng(11);
   auto size = [&](int bits) { return std::min<int64_t>(1 + (int64_t)(rng() >> (64 - 1 - rng() % bits)), (int64_t)1 << bits); };
@@ -57,6 +67,8 @@ int main() {
     a.x = a.weight = (const void*)(uintptr_t)(4096 + rng() % 2 * 4);
     a.x_ld = a.cols + rng() % 3 * 4;
     a.weight_ld = a.cols + rng() % 2;
+    const int64_t steps = size(16);
+    if (!chains(a.vocab, a.rows, steps)) { printf("%ld x %ld, %ld steps\n", (long)a.vocab, (long)a.rows, (long)steps); return 1; }
     if (!loss(a)) { printf("loss %ld %ld %ld type %d\n", (long)a.rows, (long)a.cols, (long)a.vocab, a.dtype); return 1; }
   }
   printf("ok\n");
