@@ -27,8 +27,10 @@ int launch_check(const char* what) {
 
 unsigned grid_of(int64_t want, int64_t most = 1 << 16) { return (unsigned)std::max<int64_t>(1, std::min(want, most)); }
 
-template <typename T, typename E, Form F, int WR, int WC, int FR, int FC, int NS, int KS = 1>
+template <typename T, typename E, Form F, TileKind K, int WR, int WC, int FR, int FC, int NS, int KS = 1>
 void launch_tile(const Product& p, const typename E::Args& e, hipStream_t s) {
+  static_assert(tile_r(K) == WR * FR * 32 && tile_c(K) == WC * FC * 32 && waves_r(K) == WR && threads(K) == WR * WC * KS * 64,
+                "the tile is the one that sizes, workspaces and limits were worked out for");
   const unsigned groups = (unsigned)p.tiles_r * (unsigned)p.tiles_c * (unsigned)p.slices;
   hipLaunchKernelGGL((k_product<T, WR, WC, FR, FC, NS, KS, F, E>), groups, WR * WC * KS * 64, 0, s, p, e);
 }
@@ -42,15 +44,15 @@ void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStrea
       // fewer) a fourth stage is more under way: one token through two 14336 x 4096 bf16
       // weights from memory 47.6 us against 49.5; six stages, or steps fetched in pairs,
       // gave no more.  786 tiles (50257 x 768) take 25 us with four stages, 18 with three.
-      if ((int64_t)c.tiles_r * c.tiles_c * c.slices <= 2 * kUnits) return launch_tile<T, E, F, 1, 1, 2, 1, 4>(p, e, s);
-      return launch_tile<T, E, F, 1, 1, 2, 1, 3>(p, e, s);
+      if ((int64_t)c.tiles_r * c.tiles_c * c.slices <= 2 * kUnits) return launch_tile<T, E, F, NARROW, 1, 1, 2, 1, 4>(p, e, s);
+      return launch_tile<T, E, F, NARROW, 1, 1, 2, 1, 3>(p, e, s);
     }
-  if (c.kind == WIDE) return launch_tile<T, E, F, 2, 4, 4, 2, 2>(p, e, s);
-  if (c.kind == MIDDLE) return launch_tile<T, E, F, 2, 2, 2, 2, 2>(p, e, s);
+  if (c.kind == WIDE) return launch_tile<T, E, F, WIDE, 2, 4, 4, 2, 2>(p, e, s);
+  if (c.kind == MIDDLE) return launch_tile<T, E, F, MIDDLE, 2, 2, 2, 2, 2>(p, e, s);
   // two groups of two waves: with one, half of the matrix units idle where a tile is all that a
   // compute unit has (gated block of 100 x 768 x 2048 float32 34 us against 22, bf16 with
   // gradients 35 against 33; head of 100 x 768 x 5000 with gradients 113 against 89)
-  launch_tile<T, E, F, 1, 2, 2, 1, 4, 2>(p, e, s);
+  launch_tile<T, E, F, SMALL, 1, 2, 2, 1, 4, 2>(p, e, s);
 }
 
 uint8_t* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : static_cast<uint8_t*>(workspace) + offset; }

@@ -56,6 +56,8 @@ constexpr int tile_r(TileKind k) { return k == WIDE ? 256 : k == MIDDLE ? 128 : 
 constexpr int tile_c(TileKind k) { return k == WIDE ? 256 : k == MIDDLE ? 128 : k == SMALL ? 64 : 32; }
 // waves that share a tile's rows of R: each has a part of them to itself
 constexpr int waves_r(TileKind k) { return k == WIDE || k == MIDDLE ? 2 : 1; }
+// of a workgroup (a small tile's are two groups of waves)
+constexpr int threads(TileKind k) { return k == WIDE ? 512 : k == NARROW ? 64 : 256; }
 constexpr int64_t kUnits = 256;                                 // compute units
 
 // What a product takes, in microseconds, by the times measured on the card (`steps` of

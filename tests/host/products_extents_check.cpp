@@ -1,6 +1,6 @@
 // More of the products' host half (csrc/fo_products_args.hpp) against brute force: where
-// the backward pass of the loss keeps the statistics that it makes again, and float32
-// sums of long k.
+// the backward pass of the loss keeps the statistics that it makes again, float32 sums of
+// long k, and the threads of a launch.
 #include <cstdarg>
 #include <cstdio>
 #include <random>
@@ -54,6 +54,16 @@ static bool chains(int64_t nr, int64_t nc, int64_t steps) {
   return true;
 }
 
+// A launch's threads and workgroups are 32-bit numbers.
+static bool fits(int dtype, int64_t nr, int64_t nc, int64_t steps) {
+  for (int form = 0; form < 8; ++form) {
+    const Cut c = cut(dtype, nr, nc, steps, form & 1, form & 2, form & 4);
+    const __int128 groups = (__int128)c.tiles_r * c.tiles_c * c.slices;
+    CHECK(groups >= 1 && groups < ((__int128)1 << 31) && groups * threads(c.kind) < ((__int128)1 << 32));
+  }
+  return true;
+}
+
 int main() {
   std::mt19937_64 rng(11);
   auto size = [&](int bits) { return std::min<int64_t>(1 + (int64_t)(rng() >> (64 - 1 - rng() % bits)), (int64_t)1 << bits); };
@@ -71,6 +81,19 @@ int main() {
     if (!chains(a.vocab, a.rows, steps)) { printf("%ld x %ld, %ld steps\n", (long)a.vocab, (long)a.rows, (long)steps); return 1; }
     if (!loss(a)) { printf("loss %ld %ld %ld type %d\n", (long)a.rows, (long)a.cols, (long)a.vocab, a.dtype); return 1; }
   }
+  // any two sizes that the limits allow, at and around powers of two
+  for (int dtype = 0; dtype < 3; ++dtype)
+    for (int r = 0; r <= 24; ++r)
+      for (int c = 0; c <= 24 && r + c <= 36; ++c)
+        for (int64_t odd : {-1, 0, 1})
+          for (int64_t steps : {1, 2, 11, 12, 64, 65, 1000, 1 << 15, 1 << 16}) {
+            const int64_t nr = std::max<int64_t>(1, ((int64_t)1 << r) + odd), nc = (int64_t)1 << c;
+            if (nr * nc > kMaxArea) continue;
+            if (!fits(dtype, nr, nc, steps) || !fits(dtype, nc, nr, steps)) {
+              printf("%ld x %ld, %ld steps, type %d\n", (long)nr, (long)nc, (long)steps, dtype);
+              return 1;
+            }
+          }
   printf("ok\n");
   return 0;
 }
