@@ -204,3 +204,19 @@ def test_the_library_finds_the_rest_over_several_pieces(cols):
     B.fo_loss_backward(x, w, t, lse[1:-1], one[1:2], cnt[1:2], *grads[0], rest=rest[1:-1])
     B.fo_loss_backward(x, w, t, lse[1:-1], one[1:2], cnt[1:2], *grads[1])
     assert torch.equal(grads[0][0], grads[1][0]) and torch.equal(grads[0][1], grads[1][1])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows", [20, 3000])
+def test_losses_are_not_negative(rows, dtype):
+    """log of a sum whose largest term is 1, and the target's distance from the largest logit:
+    0 at least, and 0 where nothing else counts."""
+    gen = generator(46)
+    x = torch.zeros(rows, 64, device="cuda", dtype=TYPES[dtype])
+    w = torch.zeros(300, 64, device="cuda", dtype=TYPES[dtype])
+    x[:, 0] = (1 + 999 * torch.rand(rows, generator=gen, device="cuda")).to(x.dtype)
+    w[5, 0] = 1.0
+    t = torch.full((rows,), 5, device="cuda")
+    loss = nn.linear_cross_entropy(x, w, t, reduction="none")
+    assert (loss >= 0).all()
+    assert (loss[x[:, 0] > 128] <= 24 * U).all()
