@@ -8,6 +8,8 @@
 
 #include "fo_torch.hpp"
 
+#include <ATen/MemoryOverlap.h>
+
 #include <algorithm>
 
 namespace {
@@ -331,7 +333,9 @@ Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>& outs, d
     const bool direct = flat(g) && flat(o) && g.strides() == o.strides();
     Tensor from = g, to = o;
     if (!direct) {
-      // through packed copies; in place, the copy is clipped and written back
+      // through packed copies; in place, the copy is clipped and written back (what cannot be
+      // written back is refused here, before anything is written)
+      at::assert_no_internal_overlap(o);
       from = flat(g) && g.is_contiguous() ? g : resolved(g.detach()).clone(at::MemoryFormat::Contiguous);
       to = in_place ? from : flat(o) && o.is_contiguous() ? o : at::empty(o.sizes(), o.options());
       held.push_back(from);
@@ -350,7 +354,11 @@ Tensor clip(const std::vector<Tensor>& grads, const std::vector<Tensor>& outs, d
   const Workspace ws = grad_workspace();
   check(fo_grad_clip(list.data(), static_cast<int32_t>(list.size()), static_cast<int32_t>(order), max_norm,
                      static_cast<float*>(norm.data_ptr()), ws.ptr(), ws.bytes, current_stream()));
-  for (auto& [o, t] : back) o.copy_(t);
+  {
+    // (as the kernels write the others: versions follow below, and inference tensors have none)
+    at::AutoDispatchBelowADInplaceOrView below;
+    for (auto& [o, t] : back) o.copy_(t);
+  }
   // a graph that saved one of these tensors must not be run on what it holds now
   for (const Tensor& o : outs)
     if (!o.is_inference()) o.unsafeGetTensorImpl()->bump_version();
