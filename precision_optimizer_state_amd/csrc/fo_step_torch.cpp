@@ -91,6 +91,15 @@ struct LossArgs {
 // of what their rounding left
 struct LossOut { Tensor loss, lse, count; };
 
+void check_loss(const Tensor& x, const Tensor& weight, const Tensor& target) {
+  check_x(x);
+  check_weight("weight", weight, x);
+  TORCH_CHECK_VALUE(target.scalar_type() == at::kLong, "target must be int64, got ", target.dtype());
+  TORCH_CHECK_VALUE(target.sizes() == x.sizes().slice(0, x.dim() - 1), "target has shape ", sizes(target),
+                    ", not x's without its last dimension (x has ", sizes(x), ")");
+  check_device(target);
+}
+
 LossOut loss_forward(const Tensor& x, const Tensor& weight, const Tensor& target, int64_t ignore_index, int32_t reduction,
                      double smoothing, bool keep) {
   LossArgs l(x, weight, target, ignore_index, reduction, smoothing);
@@ -124,11 +133,15 @@ struct Loss : torch::autograd::Function<Loss> {
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
     variable_list out(6);
     if (!grads[0].defined()) return out;
-    const variable_list kept = ctx->get_saved_variables();
-    const Tensor &x = kept[0], &weight = kept[1], &target = kept[2], &lse = kept[3], &count = kept[4];
+    const variable_list back = ctx->get_saved_variables();
+    const Tensor &x = back[0], &weight = back[1], &target = back[2];
     const auto args = saved(ctx);
     check_plain({&grads[0]});
+    check_loss(x, weight, target);
     LossArgs l(x, weight, target, args->ignore_index, args->which, args->smoothing);
+    const Tensor lse = kept(back[3], {2, l.a.rows}), count = args->which == FO_LOSS_MEAN ? kept(back[4], {}) : Tensor();
+    TORCH_CHECK_VALUE(grads[0].sizes() == (args->which == FO_LOSS_NONE ? target.sizes() : at::IntArrayRef()),
+                      "the loss's gradient has shape ", sizes(grads[0]));
     const Tensor dloss = packed(grads[0]);
     if (ctx->needs_input_grad(0)) out[0] = empty_like_shape(x);
     if (ctx->needs_input_grad(1)) out[1] = empty_like_shape(weight);
@@ -151,12 +164,7 @@ struct Loss : torch::autograd::Function<Loss> {
 Tensor linear_cross_entropy(const Tensor& x, const Tensor& weight, const Tensor& target, int64_t ignore_index,
                             int64_t reduction, double smoothing) {
   check_plain({&x, &weight});
-  check_x(x);
-  check_weight("weight", weight, x);
-  TORCH_CHECK_VALUE(target.scalar_type() == at::kLong, "target must be int64, got ", target.dtype());
-  TORCH_CHECK_VALUE(target.sizes() == x.sizes().slice(0, x.dim() - 1), "target has shape ", sizes(target),
-                    ", not x's without its last dimension (x has ", sizes(x), ")");
-  check_device(target);
+  check_loss(x, weight, target);
   if (at::GradMode::is_enabled() && (x.requires_grad() || weight.requires_grad())) {
     check_capture({&x, &weight});
     return Loss::apply(x, weight, target, ignore_index, reduction, smoothing);
@@ -188,6 +196,14 @@ struct GatedArgs {
 };
 
 struct GatedOut { Tensor y, g, u; };
+
+void check_gated(const Tensor& x, const Tensor& gate, const Tensor& up) {
+  check_x(x);
+  check_weight("gate_weight", gate, x);
+  check_weight("up_weight", up, x);
+  TORCH_CHECK_VALUE(gate.sizes() == up.sizes(), "gate_weight has shape ", sizes(gate), " and up_weight ", sizes(up),
+                    ": they must agree");
+}
 
 GatedOut gated_forward(const Tensor& x, const Tensor& gate, const Tensor& up, int32_t activation, bool keep) {
   GatedArgs l(x, gate, up, activation);
@@ -221,11 +237,15 @@ struct Gated : torch::autograd::Function<Gated> {
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
     variable_list out(4);
     if (!grads[0].defined()) return out;
-    const variable_list kept = ctx->get_saved_variables();
-    const Tensor &x = kept[0], &gate = kept[1], &up = kept[2], &g = kept[3], &u = kept[4];
+    const variable_list back = ctx->get_saved_variables();
+    const Tensor &x = back[0], &gate = back[1], &up = back[2];
     check_plain({&grads[0]});
+    check_gated(x, gate, up);
     GatedArgs l(x, gate, up, saved(ctx)->which);
+    const Tensor g = kept(back[3], {l.a.rows, l.a.features}), u = kept(back[4], {l.a.rows, l.a.features});
     const Rows dy(grads[0]);
+    TORCH_CHECK_VALUE(dy.rows == l.a.rows && dy.cols == l.a.features && grads[0].scalar_type() == x.scalar_type(),
+                      "the gradient is ", sizes(grads[0]), " of ", grads[0].dtype(), ", x ", sizes(x), " of ", x.dtype());
     if (ctx->needs_input_grad(0)) out[0] = empty_like_shape(x);
     if (ctx->needs_input_grad(1)) out[1] = empty_like_shape(gate);
     if (ctx->needs_input_grad(2)) out[2] = empty_like_shape(up);
@@ -248,11 +268,7 @@ struct Gated : torch::autograd::Function<Gated> {
 
 Tensor gated_linear(const Tensor& x, const Tensor& gate, const Tensor& up, int64_t activation) {
   check_plain({&x, &gate, &up});
-  check_x(x);
-  check_weight("gate_weight", gate, x);
-  check_weight("up_weight", up, x);
-  TORCH_CHECK_VALUE(gate.sizes() == up.sizes(), "gate_weight has shape ", sizes(gate), " and up_weight ", sizes(up),
-                    ": they must agree");
+  check_gated(x, gate, up);
   if (at::GradMode::is_enabled() && (x.requires_grad() || gate.requires_grad() || up.requires_grad())) {
     check_capture({&x, &gate, &up});
     return Gated::apply(x, gate, up, activation);

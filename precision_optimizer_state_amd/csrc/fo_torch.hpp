@@ -64,6 +64,22 @@ void check_device(const Tensor& t) {
                     static_cast<int>(dev));
 }
 
+// A view that torch negates when it reads it (the imaginary part of a conjugate)
+// holds the other sign in memory.
+Tensor resolved(const Tensor& t) { return t.is_neg() ? t.resolve_neg() : t; }
+
+Tensor packed(const Tensor& t) { return t.defined() ? resolved(t).contiguous() : t; }
+
+// What a backward pass kept comes back through hooks that a program may have set
+// (torch.autograd.graph.saved_tensors_hooks), as whatever these return: the kernels'
+// arguments are checked again.  Float32 of a known shape, packed:
+Tensor kept(const Tensor& t, at::IntArrayRef shape) {
+  TORCH_CHECK_VALUE(t.defined() && t.scalar_type() == at::kFloat && t.sizes() == shape, "a tensor kept for the backward pass, ",
+                    shape, " of float32, came back as ", t.defined() ? sizes(t) : "nothing");
+  check_device(t);
+  return packed(t);
+}
+
 // A tracer (make_fx, torch.jit.trace) sees the outputs' allocations and no launch.
 bool traced() {
   using Modes = c10::impl::TorchDispatchModeTLS;
@@ -98,10 +114,6 @@ void check_capture(std::initializer_list<const Tensor*> inputs) {
                 "default stream: release that graph first, or capture with inputs detached from it");
   }
 }
-
-// A view that torch negates when it reads it (the imaginary part of a conjugate)
-// holds the other sign in memory.
-Tensor resolved(const Tensor& t) { return t.is_neg() ? t.resolve_neg() : t; }
 
 // A tensor as a matrix: cols its last dimension, rows everything before.  The
 // tensor's own memory where its rows are consecutive elements at a constant
@@ -140,8 +152,6 @@ struct Rows {
 };
 
 void* address(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
-
-Tensor packed(const Tensor& t) { return t.defined() ? resolved(t).contiguous() : t; }
 
 Tensor empty_like_shape(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
