@@ -72,7 +72,9 @@ struct Dropout : torch::autograd::Function<Dropout> {
   }
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
     check_plain({&grads[0]});
-    return once({drop(grads[0], Saved::get(ctx)->key, ctx->get_saved_variables()[0]), Tensor(), Tensor()});
+    const Tensor state = ctx->get_saved_variables()[0];
+    check_key(Saved::get(ctx)->key, state);
+    return once({drop(grads[0], Saved::get(ctx)->key, state), Tensor(), Tensor()});
   }
 };
 
@@ -93,6 +95,19 @@ Tensor dropout(const Tensor& x, double p, uint64_t seed, uint64_t offset, const 
 // ---------------------------------------------------------------------------
 // norms
 // ---------------------------------------------------------------------------
+void check_row(const Tensor& x) {
+  TORCH_CHECK_VALUE(x.dim() > 0 && x.size(-1) > 0,
+                    "a norm needs a last dimension of at least one element, got shape ", sizes(x));
+  check_device(x);
+  dtype_of(x);
+}
+void check_param(const char* name, const Tensor& t, const Tensor& x) {
+  if (!t.defined()) return;
+  TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == x.size(-1), name, " has shape ", sizes(t), ", not [", x.size(-1), "]");
+  check_device(t);
+  dtype_of(t);
+}
+
 struct Forward {
   Tensor h, y, stats;     // stats: rstd of every row, then (layer norm) the means
 };
@@ -146,12 +161,21 @@ struct Norm : torch::autograd::Function<Norm> {
 
   static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
     const variable_list saved = ctx->get_saved_variables();
-    const Tensor &h = saved[0], &weight = saved[1], &stats = saved[2], &state = saved[3];
+    const Tensor &h = saved[0], &weight = saved[1], &state = saved[3];
     const auto args = Saved::get(ctx);
     const Key& key = args->key;
     const bool join = grads.size() == 2;
     const Tensor dy = grads.back(), dh = join ? grads[0] : Tensor();
     check_plain({&dy, &dh});
+    check_key(key, state);
+    check_row(h);
+    check_param("weight", weight, h);
+    TORCH_CHECK_VALUE(!weight.defined() || args->bias_dtype == at::ScalarType::Undefined ||
+                          weight.scalar_type() == args->bias_dtype,
+                      "weight is ", weight.dtype(), " and bias ", args->bias_dtype, ": they must agree");
+    for (const Tensor& g : {dy, dh})
+      TORCH_CHECK_VALUE(!g.defined() || (g.sizes() == h.sizes() && g.scalar_type() == h.scalar_type()), "a gradient is ",
+                        sizes(g), " of ", g.dtype(), ", the rows ", sizes(h), " of ", h.dtype());
     // the inputs that were there, in the order of forward's arguments
     size_t input = 0;
     const bool need_x = ctx->needs_input_grad(input++);
@@ -166,6 +190,7 @@ struct Norm : torch::autograd::Function<Norm> {
       return once(std::move(out));
     }
     const Rows rh(h), rdy(dy);
+    const Tensor stats = kept(saved[2], {args->kind == FO_LAYER_NORM ? 2 : 1, rh.rows});
     std::optional<Rows> rdh;
     if (dh.defined()) rdh.emplace(dh);
     // without dropout the gradients of x and of the residual are one tensor
@@ -219,17 +244,11 @@ variable_list norm(const Tensor& x, const MaybeTensor& residual_arg, const Maybe
   const Tensor state = value(state_arg);
   check_key(key, state);
   check_plain({&x, &residual, &weight, &bias});
-  TORCH_CHECK_VALUE(x.dim() > 0 && x.size(-1) > 0,
-                    "a norm needs a last dimension of at least one element, got shape ", sizes(x));
-  check_device(x);
-  dtype_of(x);
+  check_row(x);
   bool grad = x.requires_grad();
   for (const auto& [name, t] : {std::pair<const char*, const Tensor&>{"weight", weight}, {"bias", bias}}) {
-    if (!t.defined()) continue;
-    TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == x.size(-1), name, " has shape ", sizes(t), ", not [", x.size(-1), "]");
-    check_device(t);
-    dtype_of(t);
-    grad |= t.requires_grad();
+    check_param(name, t, x);
+    grad |= t.defined() && t.requires_grad();
   }
   if (weight.defined() && bias.defined())
     TORCH_CHECK_VALUE(weight.scalar_type() == bias.scalar_type(), "weight is ", weight.dtype(), " and bias ",
