@@ -132,7 +132,8 @@ inline double cut_time(int dtype, const Cut& c, int64_t steps) {
 }
 
 // Vocabulary per piece of the backward pass: the logits' gradients of a piece are at
-// most about 2^28 elements (512 MB in 16 bits).  Of the sizes down to half of that the
+// most 2^28 elements (512 MB in 16 bits), and a little padding, or 1024 places of every
+// token where that is more (past 2^18 tokens).  Of the sizes down to half of that the
 // one whose three products fill the card's last rounds best (8192 tokens, 768 columns,
 // 50257 places: 21504 instead of 25344, whose weight gradients are 297 wide tiles on 256
 // compute units).  Where there are several they are multiples of 256: whole tiles of any kind.

@@ -79,7 +79,8 @@ def clip_grads(grads, max_norm: float, norm_type: float = 2.0, *, out=None, erro
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
                     error_if_nonfinite: bool = False) -> torch.Tensor:
     """torch.nn.utils.clip_grad_norm_ on clip_grads(): scale the .grad of
-    `parameters` in place; returns the norm before clipping.  Gradients are left
-    untouched, and unwritten, where the bound holds."""
+    `parameters` in place; returns the norm before clipping.  Where the bound holds
+    gradients keep their bits, and are not written unless they are slices that are not
+    one stretch of memory: those are clipped as copies and written back."""
     grads = [p.grad for p in _listed(parameters) if p.grad is not None]
     return clip_grads(grads, max_norm, norm_type, error_if_nonfinite=error_if_nonfinite)[1]

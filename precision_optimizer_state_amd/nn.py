@@ -211,7 +211,8 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
     loss and gradients NaN.  The loss is float32: a scalar ("mean", over the counted
     tokens, or "sum") or one per token ("none").  The backward pass computes the
     logits again, a piece of the vocabulary at a time; their gradients are rounded
-    to x's type on the way to those of x and weight."""
+    to x's type on the way to those of x and weight.  8 bytes per token are kept for
+    it: log sum exp as two floats, so that probabilities are right at any size of logits."""
     if reduction not in B.REDUCTION:
         raise ValueError(f"reduction must be one of {', '.join(B.REDUCTION)}, got {reduction!r}")
     if not 0.0 <= label_smoothing <= 1.0:
@@ -225,7 +226,8 @@ def gated_linear(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Te
     """act(x gate_weight^T) * (x up_weight^T), the first half of a gated
     feed-forward block, in one kernel.  x: (..., cols), weights: (features, cols),
     all of one type; activation: "silu", "gelu" or "gelu_tanh".  For the backward
-    pass the two products are kept in float32 (8 bytes per output element)."""
+    pass the two products are kept in float32 (8 bytes per output element: more than
+    layers of 16 bits keep)."""
     if activation not in B.ACTIVATION:
         raise ValueError(f"activation must be one of {', '.join(B.ACTIVATION)}, got {activation!r}")
     return (_loaded_step or _step_ext()).gated_linear(x, gate_weight, up_weight, B.ACTIVATION[activation])
