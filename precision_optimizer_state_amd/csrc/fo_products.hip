@@ -217,8 +217,8 @@ int run_loss_backward(const fo_loss* a, const float* rest, const LossBackward& b
     const Operand dz = {at(ws, b.dz), nvp + kGap};
     const Product pz = product_of(w, nv, x, a->rows, b.k, es);
     // tokens in whole steps: the padding is written too (as zeros)
-    launch_product<T, LogitGradients, ROWS_ROWS, false>(
-        pz, cut(a->dtype, nv, b.n, pz.steps, false, false, false),
+    launch_product<T, LogitGradients, ROWS_ROWS, true>(
+        pz, b.logits(nv, a->rows),
         {at(ws, b.dz), dz.ld, a->lse, rest, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
          (float)a->smoothing}, s);
     if (a->dx) {

@@ -82,6 +82,10 @@ inline double product_time(TileKind k, bool f32, int64_t tiles, int64_t slices, 
          (last ? round_time(k, f32, k != WIDE && last <= kUnits, each) : 0.0);
 }
 
+inline Cut tiles_of(TileKind k, int64_t nr, int64_t nc) {
+  return {k, (int)((nr + tile_r(k) - 1) / tile_r(k)), (int)((nc + tile_c(k) - 1) / tile_c(k)), 1};
+}
+
 // How nr (with `dual`, of each of two matrices) rows of R against nc of C, `steps` of k,
 // are cut: the kind of tile, and with `sliced` the number of slices of k (whose sums are
 // written and read once more, 4 bytes each way at 5 TB/s), that take the least time.
@@ -89,9 +93,7 @@ inline double product_time(TileKind k, bool f32, int64_t tiles, int64_t slices, 
 inline Cut cut(int dtype, int64_t nr, int64_t nc, int64_t steps, bool dual, bool narrow_ok, bool sliced) {
   const int64_t all_r = dual ? 2 * up(nr, 32) : nr;
   const bool f32 = dtype == FO_F32;
-  auto tiles = [&](TileKind k) {
-    return Cut{k, (int)((all_r + tile_r(k) - 1) / tile_r(k)), (int)((nc + tile_c(k) - 1) / tile_c(k)), 1};
-  };
+  auto tiles = [&](TileKind k) { return tiles_of(k, all_r, nc); };
   // at most 32, and 1 GB of sums
   const int64_t most = sliced ? std::max<int64_t>(1, std::min<int64_t>(32, (int64_t(1) << 28) / (nr * nc))) : 1;
   auto slices = [&](Cut c) {
@@ -138,14 +140,15 @@ inline double cut_time(int dtype, const Cut& c, int64_t steps) {
 // 50257 places: 21504 instead of 25344, whose weight gradients are 297 wide tiles on 256
 // compute units).  Where there are several they are multiples of 256: whole tiles of any kind.
 constexpr int64_t kPieceElems = int64_t(1) << 28;
-inline int64_t piece_vocab(int dtype, int64_t tokens, int64_t cols, int64_t vocab) {
+// (`kind`: of the tiles that make the logits)
+inline int64_t piece_vocab(int dtype, int64_t tokens, int64_t cols, int64_t vocab, TileKind kind) {
   const int64_t es = (int64_t)elem_size(dtype), n = padded(tokens);
   const int64_t most = std::min(std::max<int64_t>(1024, kPieceElems / n / 256 * 256), kMaxRowBytes / 4);
   if (vocab <= most) return padded(vocab);
   const int64_t steps_d = (cols * es + 127) / 128, steps_n = n * es / 128;
   auto time = [&](int64_t nv) {
     const int64_t steps_v = padded(nv) * es / 128;
-    return cut_time(dtype, cut(dtype, nv, n, steps_d, false, false, false), steps_d) +
+    return cut_time(dtype, tiles_of(kind, nv, n), steps_d) +
            cut_time(dtype, cut(dtype, cols, tokens, steps_v, false, true, true), steps_v) +
            cut_time(dtype, cut(dtype, cols, nv, steps_n, false, true, false), steps_n);
   };
@@ -185,9 +188,18 @@ inline LossForward loss_forward(const fo_loss* a) {
 
 struct LossBackward {
   int64_t unit = -1, factor = -1, rest = -1, x = -1, w = -1, xm = -1, dz = -1, sums = -1, bytes = 0;
+  // The forward pass's tiles.  The logits are made again in tiles of the same kind, whose sums
+  // add up in the same order: the same bits, so that what they are off by cancels in exp(z - lse).
+  // (With tiles chosen for themselves, small ones for the narrow tiles of 32 tokens and fewer, float32
+  // gradients of 22 x 386 x 13 were off by 6e-6 instead of 2e-7, and probabilities added up to 1 only
+  // as well as two ways of adding a logit agree.)
+  Cut statistics = {};
   // without the forward pass's `rest`: its statistics again, where dz comes later
   int64_t part = -1, parts = 0;
-  Cut statistics = {};
+  // tiles of a piece of nv places: all tokens of whole steps, or of a narrow tile
+  Cut logits(int64_t nv, int64_t rows) const {
+    return tiles_of(statistics.kind, nv, statistics.kind == NARROW ? rows : n);
+  }
   int64_t k, n, piece, sums_ld;                                 // columns and tokens in whole steps; vocabulary per piece
   Cut dx = {};                                                  // of a whole piece
 };
@@ -197,7 +209,8 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   const int64_t es = (int64_t)elem_size(a->dtype);
   b.k = a->cols % (128 / es) ? padded(a->cols) : a->cols;
   b.n = padded(a->rows);
-  b.piece = piece_vocab(a->dtype, a->rows, a->cols, a->vocab);
+  b.statistics = cut(a->dtype, a->vocab, a->rows, b.k * es / 128, false, true, false);
+  b.piece = piece_vocab(a->dtype, a->rows, a->cols, a->vocab, b.statistics.kind);
   if (a->reduction == FO_LOSS_NONE) {
     b.unit = l.take(a->rows * 4);
     b.factor = l.take(4);
@@ -206,7 +219,6 @@ inline LossBackward loss_backward(const fo_loss* a, bool dx, bool dw) {
   if (!direct(a->weight, a->vocab, a->cols, a->weight_ld, a->dtype)) b.w = l.take(std::min(b.piece, a->vocab) * b.k * es);
   if (dw) b.xm = l.take(b.n * b.k * es);
   b.rest = l.take(a->rows * 4);
-  b.statistics = cut(a->dtype, a->vocab, a->rows, b.k * es / 128, false, true, false);
   b.parts = (int64_t)waves_r(b.statistics.kind) * b.statistics.tiles_r;
   b.part = b.dz = l.take(std::max(b.n * (b.piece + kGap) * es, b.parts * a->rows * 8));
   b.sums_ld = up(a->cols, 4);

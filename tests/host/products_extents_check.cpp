@@ -30,6 +30,13 @@ static bool loss(const fo_loss& a) {
       const int64_t nv = std::min(b.piece, a.vocab - first), tile = tile_r(b.statistics.kind);
       CHECK(first / tile == tiles);
       tiles += (nv + tile - 1) / tile;
+      // the logits again: the same kind of tile, each of which begins at a token that is there, and
+      // which reach all tokens' whole steps (a narrow one writes its step's other half itself)
+      const Cut c = b.logits(nv, a.rows);
+      CHECK(c.kind == f.c.kind && c.slices == 1 && c.tiles_r == (nv + tile - 1) / tile);
+      CHECK((int64_t)(c.tiles_c - 1) * tile_c(c.kind) < a.rows);
+      CHECK(c.kind == NARROW ? a.rows <= 32 && b.n == 64 && c.tiles_c == 1 : (int64_t)c.tiles_c * tile_c(c.kind) >= b.n);
+      CHECK((__int128)c.tiles_r * c.tiles_c * threads(c.kind) < ((__int128)1 << 32));
     }
     CHECK(tiles == f.c.tiles_r && b.parts == tiles * waves_r(f.c.kind));
     // (gradients of logits take that place afterwards)

@@ -17,7 +17,7 @@ import torch
 
 from precision_optimizer_state_amd import binding as B
 from precision_optimizer_state_amd import nn
-from step_helpers import TYPES, U, check, generator, half_step, product_bound
+from step_helpers import TYPES, U, check, generator, half_step, normal, product_bound
 from test_gpu_loss import make, run
 
 pytestmark = pytest.mark.gpu
@@ -220,3 +220,25 @@ def test_losses_are_not_negative(rows, dtype):
     loss = nn.linear_cross_entropy(x, w, t, reduction="none")
     assert (loss >= 0).all()
     assert (loss[x[:, 0] > 128] <= 24 * U).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows, vocab", [(1, 50), (20, 13), (32, 2000), (33, 300), (100, 5000), (400, 700), (1100, 5001)])
+def test_probabilities_add_up_to_one(rows, vocab, dtype):
+    """The backward pass makes the forward pass's logits to the bit, so that the roundings of
+    sums of many large terms cancel: a column of ones in the weight gives the sum of a
+    token's gradients of logits, which is 0.  It is off by E and 2 U (1.45 D + 4) for the
+    probabilities (D e^-D is at most 0.4), their roundings to the type, and the product's
+    own, of at most 2 in absolute values."""
+    gen = generator(48)
+    cols, E = 513, (2 * (2 * (1.45 * 0.4 + 4)) + vocab / 4096 + 200 + 4 * (1 + math.log(vocab)))
+    x = normal(gen, rows, cols, dtype=TYPES[dtype], scale=60.0)
+    w = normal(gen, vocab, cols, dtype=TYPES[dtype])
+    x[:, 512], w[:, 512] = 0.0, 1.0
+    t = torch.randint(vocab, (rows,), generator=gen, device="cuda")
+    _, dx, _, _ = run(x, w, t, "none")
+    half = 0.0 if dtype == "f32" else torch.finfo(TYPES[dtype]).eps / 2
+    # (float32 sums of V terms of at most 2 in all, in matrix instructions: 2 (V + 40) U of that, of which
+    # the terms that are not 0 are a few)
+    room = (E + 2 * 64 * 2) * U + 2 * half + 2.0 ** -24
+    assert dx[:, 512].abs().max() <= room
