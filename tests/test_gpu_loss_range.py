@@ -223,6 +223,16 @@ def test_losses_are_not_negative(rows, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("smoothing", [0.0, 0.25, 1.0])
+@pytest.mark.parametrize("rows", [1, 19, 324])
+def test_a_vocabulary_of_one_place(rows, smoothing, dtype):
+    """The softmax of one logit is 1, whatever the logit: no loss and no gradients, exactly."""
+    x, w, t = make(47, rows, 80, 1, dtype)
+    loss, dx, dw, _ = run(x, w, t, "none", smoothing)
+    assert not loss.any() and not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows, vocab", [(1, 50), (20, 13), (32, 2000), (33, 300), (100, 5000), (400, 700), (1100, 5001)])
 def test_probabilities_add_up_to_one(rows, vocab, dtype):
     """The backward pass makes the forward pass's logits to the bit, so that the roundings of
