@@ -35,18 +35,17 @@ void launch_tile(const Product& p, const typename E::Args& e, hipStream_t s) {
   hipLaunchKernelGGL((k_product<T, WR, WC, FR, FC, NS, KS, F, E>), groups, WR * WC * KS * 64, 0, s, p, e);
 }
 
-template <typename T, typename E, Form F, bool NARROW_OK>
+template <typename T, typename E, Form F>
 void launch_product(Product p, const Cut& c, const typename E::Args& e, hipStream_t s) {
   p.tiles_r = c.tiles_r; p.tiles_c = c.tiles_c; p.slices = c.slices;
-  if constexpr (NARROW_OK)
-    if (c.kind == NARROW) {
-      // three stages let four workgroups share a compute unit; where two do (512 tiles and
-      // fewer) a fourth stage is more under way: one token through two 14336 x 4096 bf16
-      // weights from memory 47.6 us against 49.5; six stages, or steps fetched in pairs,
-      // gave no more.  786 tiles (50257 x 768) take 25 us with four stages, 18 with three.
-      if ((int64_t)c.tiles_r * c.tiles_c * c.slices <= 2 * kUnits) return launch_tile<T, E, F, NARROW, 1, 1, 2, 1, 4>(p, e, s);
-      return launch_tile<T, E, F, NARROW, 1, 1, 2, 1, 3>(p, e, s);
-    }
+  if (c.kind == NARROW) {
+    // three stages let four workgroups share a compute unit; where two do (512 tiles and
+    // fewer) a fourth stage is more under way: one token through two 14336 x 4096 bf16
+    // weights from memory 47.6 us against 49.5; six stages, or steps fetched in pairs,
+    // gave no more.  786 tiles (50257 x 768) take 25 us with four stages, 18 with three.
+    if ((int64_t)c.tiles_r * c.tiles_c * c.slices <= 2 * kUnits) return launch_tile<T, E, F, NARROW, 1, 1, 2, 1, 4>(p, e, s);
+    return launch_tile<T, E, F, NARROW, 1, 1, 2, 1, 3>(p, e, s);
+  }
   if (c.kind == WIDE) return launch_tile<T, E, F, WIDE, 2, 4, 4, 2, 2>(p, e, s);
   if (c.kind == MIDDLE) return launch_tile<T, E, F, MIDDLE, 2, 2, 2, 2, 2>(p, e, s);
   // two groups of two waves: with one, half of the matrix units idle where a tile is all that a
@@ -156,7 +155,7 @@ int run_loss_forward(const fo_loss* a, float* rest, const LossForward& f, hipStr
   float* chosen = (float*)at(a->workspace, f.chosen);
   float* each = reduced ? (float*)at(a->workspace, f.each) : a->loss;
   const Product p = product_of(w, a->vocab, x, a->rows, f.k, es);
-  launch_product<T, Statistics, ROWS_ROWS, true>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
+  launch_product<T, Statistics, ROWS_ROWS>(p, f.c, {part, sums, chosen, a->target, a->ignore_index}, s);
   join_rows({part, sums, chosen, a->target, each, a->lse, nullptr, rest, a->ignore_index, (int)a->rows,
              waves_r(f.c.kind) * f.c.tiles_r, (int)a->vocab, 1, (float)a->smoothing}, s);
   if (reduced)
@@ -179,7 +178,7 @@ const float* find_rest(const fo_loss* a, const LossBackward& b, const Operand& x
     pack.launch(s);
     Cut c = b.statistics;
     c.tiles_r = (int)((nv + tile - 1) / tile);
-    launch_product<T, Statistics, ROWS_ROWS, true>(
+    launch_product<T, Statistics, ROWS_ROWS>(
         product_of(w, nv, x, a->rows, b.k, es), c,
         {part + first / tile * waves_r(c.kind) * a->rows, nullptr, nullptr, a->target, a->ignore_index}, s);
   }
@@ -217,7 +216,7 @@ int run_loss_backward(const fo_loss* a, const float* rest, const LossBackward& b
     const Operand dz = {at(ws, b.dz), nvp + kGap};
     const Product pz = product_of(w, nv, x, a->rows, b.k, es);
     // tokens in whole steps: the padding is written too (as zeros)
-    launch_product<T, LogitGradients, ROWS_ROWS, true>(
+    launch_product<T, LogitGradients, ROWS_ROWS>(
         pz, b.logits(nv, a->rows),
         {at(ws, b.dz), dz.ld, a->lse, rest, unit, a->target, a->ignore_index, (int)first, (int)a->vocab, (int)b.n, scale,
          (float)a->smoothing}, s);
@@ -225,14 +224,14 @@ int run_loss_backward(const fo_loss* a, const float* rest, const LossBackward& b
       Product px = product_of(w, a->cols, dz, a->rows, nvp, es);
       px.k = (int)nv;
       if (b.sums >= 0)
-        launch_product<T, KeepSums, COLS_ROWS, true>(px, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
+        launch_product<T, KeepSums, COLS_ROWS>(px, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, first > 0}, s);
       else
-        launch_product<T, StoreScaled, COLS_ROWS, true>(
+        launch_product<T, StoreScaled, COLS_ROWS>(
             px, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, factor, 1.0f / scale, a->target, a->ignore_index}, s);
     }
     if (a->dweight) {
       const Product pw = product_of(xm, a->cols, dz, nv, b.n, es);
-      launch_product<T, StoreScaled, COLS_COLS, true>(
+      launch_product<T, StoreScaled, COLS_COLS>(
           pw, cut(a->dtype, a->cols, nv, pw.steps, false, true, false),
           {static_cast<uint8_t*>(a->dweight) + first * a->cols * es, nullptr, (int)nv, (int)nv, 0, a->cols, factor,
            1.0f / scale, nullptr, 0}, s);
@@ -283,7 +282,7 @@ int run_gated_forward(const fo_gated* a, const GatedForward& f, hipStream_t s) {
   pack.launch(s);
   Product p = product_of(gate, a->features, x, a->rows, f.k, es);
   p.r2 = up_w.p;
-  launch_product<T, Gated, DUAL_ROWS, true>(p, f.c, {a->y, a->g, a->u, a->activation}, s);
+  launch_product<T, Gated, DUAL_ROWS>(p, f.c, {a->y, a->g, a->u, a->activation}, s);
   return launch_check("gated forward launch");
 }
 
@@ -307,18 +306,18 @@ int run_gated_backward(const fo_gated* a, const GatedBackward& b, hipStream_t s)
     p.joint = (int)(half * es / 128);
     if (b.dx.slices > 1) {
       const int64_t slice = a->rows * b.sums_ld;
-      launch_product<T, KeepSums, COLS_ROWS, true>(p, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, 0}, s);
+      launch_product<T, KeepSums, COLS_ROWS>(p, b.dx, {(float*)at(ws, b.sums), b.sums_ld, slice, 0}, s);
       const JoinArgs j = {(const float*)at(ws, b.sums), b.sums_ld, slice, b.dx.slices, a->dx, {nullptr, nullptr}, nullptr, 0,
                           (int)a->rows, (int)a->cols, 1.0f};
       hipLaunchKernelGGL((k_join<T>), grid_of((slice / 4 + 255) / 256), 256, 0, s, j);
     } else {
-      launch_product<T, StoreScaled, COLS_ROWS, true>(p, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, {nullptr, nullptr}, 1.0f, nullptr, 0}, s);
+      launch_product<T, StoreScaled, COLS_ROWS>(p, b.dx, {a->dx, nullptr, (int)a->rows, (int)a->rows, 0, a->cols, {nullptr, nullptr}, 1.0f, nullptr, 0}, s);
     }
   }
   if (a->dgate || a->dup) {
     Product p = product_of(x, a->cols, d, 2 * half, b.n, es);
     p.k = (int)a->rows;
-    launch_product<T, StoreScaled, COLS_COLS, true>(
+    launch_product<T, StoreScaled, COLS_COLS>(
         p, cut(a->dtype, a->cols, 2 * half, p.steps, false, true, false),
         {a->dgate, a->dup, (int)half, (int)a->features, (int)a->features, a->cols, {nullptr, nullptr}, 1.0f, nullptr, 0}, s);
   }

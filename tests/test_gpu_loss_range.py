@@ -122,9 +122,8 @@ def test_one_place_or_two_that_dominate(dtype, places):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_logits_that_depend_on_their_order_of_summation(dtype):
-    """Sums of many large terms differ by whole numbers between two ways of adding them, and
-    the backward pass may add in another way than the forward pass.  Gradients of logits
-    stay in [-1, 1] all the same."""
+    """Sums of many large terms differ by whole numbers between two ways of adding them.
+    Gradients of logits stay in [-1, 1] all the same."""
     gen = generator(42)
     for rows in (20, 100, 400):
         x = (1e5 * torch.randn(rows, 256, generator=gen, device="cuda")).to(TYPES[dtype])
